@@ -77,7 +77,11 @@ enum {
   GQE_OP_COMBINE_OUT_PROJ = 3,
   GQE_OP_ATTN_BWD = 4,
   GQE_OP_LAYER_FORWARD = 5,       /* gqe_layer_forward */
-  GQE_OP_LAYER_FORWARD_HOST = 6   /* gqe_layer_forward_host; dims->B = sequences per chunk */
+  GQE_OP_LAYER_FORWARD_HOST = 6,  /* gqe_layer_forward_host; dims->B = sequences per chunk */
+  /* sized by gqe_window_workspace_size */
+  GQE_OP_ATTN_WINDOW_BWD = 7,     /* gqe_attn_prefill_window_bwd */
+  GQE_OP_ATTN_DECODE_WINDOW = 8,  /* gqe_attn_decode_window */
+  GQE_OP_ATTN_TREE = 9            /* gqe_attn_tree */
 };
 
 /* Bytes of scratch the call `op` needs for these dims (L_max: the decode
@@ -170,6 +174,96 @@ gqe_status gqe_attn_prefill_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, 
                                 const gqe_bf16* o_sh, const float* lse, const gqe_bf16* do_routed,
                                 const gqe_bf16* do_sh, gqe_bf16* dq_routed, gqe_bf16* dq_sh, gqe_bf16* dK,
                                 gqe_bf16* dV, void* ws, size_t ws_bytes, gqe_stream stream);
+
+/* Sliding window with sinks.  The calls below bound what a query sees: the
+ * query of a token at position t sees key p when
+ *   p <= t  and  (p > t - window  or  p < sinks),
+ * the last `window` tokens up to its own and the first `sinks` tokens of the
+ * sequence.  window 0 means no bound (sinks then add nothing).  The rows,
+ * layouts, scale, shared head and fp32 accumulation are those of the calls
+ * without a window; GQE's pages describe full causal attention only, so these
+ * are its calls over a smaller set of keys.
+ * K, V and cache rows that some query of the call sees must be finite; rows
+ * that no query of the call sees (past a length, or between the sinks and the
+ * first query's window) may hold anything in the decode and tree calls. */
+
+/* gqe_attn_prefill under a window.  window >= 0, sinks >= 0; the other
+ * arguments and the outputs are those of gqe_attn_prefill.  A window of 0 or
+ * of at least T gives gqe_attn_prefill's result bit for bit. */
+gqe_status gqe_attn_prefill_window(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                   const gqe_bf16* K, const gqe_bf16* V, int window, int sinks, gqe_bf16* o_routed,
+                                   gqe_bf16* o_sh, float* lse, gqe_stream stream);
+
+/* Backward of gqe_attn_prefill_window for the same window and sinks; the other
+ * arguments are those of gqe_attn_prefill_bwd (o and lse from
+ * gqe_attn_prefill_window).  dK and dV do not depend on timing; dq is summed
+ * over key tiles in an order that may differ between runs.
+ *   ws: gqe_window_workspace_size(GQE_OP_ATTN_WINDOW_BWD) bytes, 256-byte
+ *   aligned. */
+gqe_status gqe_attn_prefill_window_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                       const gqe_bf16* K, const gqe_bf16* V, int window, int sinks,
+                                       const gqe_bf16* o_routed, const gqe_bf16* o_sh, const float* lse,
+                                       const gqe_bf16* do_routed, const gqe_bf16* do_sh, gqe_bf16* dq_routed,
+                                       gqe_bf16* dq_sh, gqe_bf16* dK, gqe_bf16* dV, void* ws, size_t ws_bytes,
+                                       gqe_stream stream);
+
+/* gqe_attn_decode under a window: the new token is at position
+ * cache_len[b] - 1 and reads only the cache rows it sees, so the call's cost
+ * does not grow with the cache.  The other arguments are those of
+ * gqe_attn_decode, out-of-range cache lengths included.
+ *   ws: gqe_window_workspace_size(GQE_OP_ATTN_DECODE_WINDOW) bytes (NULL when
+ *   that is 0), 16-byte aligned. */
+gqe_status gqe_attn_decode_window(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                  const gqe_bf16* Kc, const gqe_bf16* Vc, int L_max, const int32_t* cache_len,
+                                  int window, int sinks, gqe_bf16* o_routed, gqe_bf16* o_sh, void* ws,
+                                  size_t ws_bytes, gqe_stream stream);
+
+/* Attention of a tree of drafted tokens (speculative decoding): dims->T <= 128
+ * drafted tokens per sequence against the dense cache and one another, in one
+ * softmax.  Their K and V rows stay apart from the cache, which is not written.
+ *   q_routed [B, G, T, k, d], q_sh [B, T, d] as gqe_routed_qproj writes them;
+ *   Kt, Vt [B, G, T, d] as gqe_kv_proj writes them for the B*T drafted tokens.
+ *   parent [B, T] int32: parent[b, i] in [-1, i) is the drafted token that
+ *     token i follows, -1 when it follows the cache's last row.  Token i sits
+ *     at position cache_len[b] + depth(i), its depth the number of drafted
+ *     tokens above it, and sees of the drafted tokens the ones above it and
+ *     itself.  A chain (parent[b, i] = i - 1) is a causal chunk of T tokens.
+ *   tree_len [B] int32 in [0, T], or NULL for T everywhere: sequence b drafts
+ *     tokens 0 .. tree_len[b]-1; the rows past them get zero outputs, and
+ *     their q, Kt, Vt and parent are not used.
+ *   Kc, Vc [B, G, L_max, d]; cache_len [B] int32 in [0, L_max]: cache rows
+ *     before the drafted tokens (the new tokens not included).
+ *   window, sinks: as above, over positions (cache rows and drafted tokens).
+ *   o_routed [B, G, T, k, d], o_sh [B, T, d].
+ *   ws: gqe_window_workspace_size(GQE_OP_ATTN_TREE) bytes (NULL when that is
+ *   0), 16-byte aligned.
+ * A value outside its range is a caller error the device detects: code 0x302
+ * (cache_len) or 0x304 (tree_len, parent) in the device error word; lengths
+ * are clamped and a bad parent counts as -1.
+ * Errors: GQE_ERR_UNSUPPORTED for T > 128, else as gqe_attn_decode. */
+gqe_status gqe_attn_tree(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh, const gqe_bf16* Kt,
+                         const gqe_bf16* Vt, const int32_t* parent, const int32_t* tree_len, const gqe_bf16* Kc,
+                         const gqe_bf16* Vc, int L_max, const int32_t* cache_len, int window, int sinks,
+                         gqe_bf16* o_routed, gqe_bf16* o_sh, void* ws, size_t ws_bytes, gqe_stream stream);
+
+/* Moves the accepted drafted tokens to the end of the cache: for i <
+ * n_accept[b], cache row cache_len[b] + i of every group becomes drafted row
+ * path[b, i], and new_len[b] = cache_len[b] + n_accept[b].  new_len may be
+ * cache_len itself; nothing else of the cache is written.
+ *   Kt, Vt [B, G, T, d] (T <= 128), path [B, T] int32 (entries past
+ *   n_accept[b] are not used), n_accept [B] int32 in [0, T], Kc, Vc
+ *   [B, G, L_max, d], cache_len [B] int32 in [0, L_max].
+ * Out of range (code 0x305 in the device error word): lengths are clamped,
+ * rows that do not fit the cache are dropped (new_len is then L_max), and a
+ * path entry outside [0, T) leaves its cache row as it was. */
+gqe_status gqe_cache_commit(const gqe_dims* dims, const gqe_bf16* Kt, const gqe_bf16* Vt, const int32_t* path,
+                            const int32_t* n_accept, gqe_bf16* Kc, gqe_bf16* Vc, int L_max, const int32_t* cache_len,
+                            int32_t* new_len, gqe_stream stream);
+
+/* Bytes of scratch of the windowed and tree calls: op GQE_OP_ATTN_WINDOW_BWD,
+ * GQE_OP_ATTN_DECODE_WINDOW (dims->T = 1) or GQE_OP_ATTN_TREE, L_max the cache
+ * length (the last two).  May be 0.  Errors as the calls themselves. */
+gqe_status gqe_window_workspace_size(const gqe_dims* dims, int op, int L_max, int window, int sinks, size_t* bytes);
 
 /* C [M, N] = sum_k A(m, k) B(n, k), bf16 in and out, fp32 accumulation on
  * tcgen05 (the projections of the backward pass).  Operand layouts:
@@ -386,9 +480,11 @@ gqe_status gqe_layer_forward_host(const gqe_dims* dims, const gqe_layer_weights*
 
 /* Reads and clears the device error word (0 = none).  Kernels set it when one
  * of their internal waits runs out of time (0x101 GEMM, 0x201 attention,
- * 0x202 attention backward, 0x301 decode, 0x401 router, 0x7F1 the failure
- * check below) and when gqe_attn_decode meets a cache_len outside
- * [1, L_max] (0x302).  The first code recorded is kept.  Synchronises
+ * 0x202 attention backward, 0x301 decode, 0x303 tree and windowed decode,
+ * 0x401 router, 0x7F1 the failure check below), when a decode or tree call
+ * meets a cache_len outside its range (0x302), gqe_attn_tree a tree_len or
+ * parent outside its range (0x304) or gqe_cache_commit a value outside its
+ * range (0x305).  The first code recorded is kept.  Synchronises
  * `stream`. */
 gqe_status gqe_device_error(int* code, gqe_stream stream);
 

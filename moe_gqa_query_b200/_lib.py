@@ -26,6 +26,9 @@ GQE_OP_COMBINE_OUT_PROJ = 3
 GQE_OP_ATTN_BWD = 4
 GQE_OP_LAYER_FORWARD = 5
 GQE_OP_LAYER_FORWARD_HOST = 6
+GQE_OP_ATTN_WINDOW_BWD = 7
+GQE_OP_ATTN_DECODE_WINDOW = 8
+GQE_OP_ATTN_TREE = 9
 STATUS_NAMES = {0: "GQE_OK", 1: "GQE_ERR_INVALID_ARG", 2: "GQE_ERR_UNSUPPORTED",
                 3: "GQE_ERR_WORKSPACE", 4: "GQE_ERR_CUDA", 5: "GQE_ERR_DEVICE_CHECK"}
 
@@ -78,6 +81,12 @@ SIGNATURES = {
     "gqe_attn_prefill_bwd": [_D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
     "gqe_attn_decode": [_D, _P, _P, _P, _P, _I, _P, _P, _P, _P, _SZ, _P],
     "gqe_attn_decode_noalloc": [_D, _P, _P, _P, _P, _I, _P, _P, _P, _P],
+    "gqe_attn_prefill_window": [_D, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P],
+    "gqe_attn_prefill_window_bwd": [_D, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+    "gqe_attn_decode_window": [_D, _P, _P, _P, _P, _I, _P, _I, _I, _P, _P, _P, _SZ, _P],
+    "gqe_attn_tree": [_D, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _P, _P, _P, _SZ, _P],
+    "gqe_cache_commit": [_D, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P],
+    "gqe_window_workspace_size": [_D, _I, _I, _I, _I, ctypes.POINTER(_SZ)],
     "gqe_combine": [_D, _P, _P, _P, _P, _P],
     "gqe_combine_out_proj": [_D, _P, _P, _P, _P, _P, _P, _SZ, _P],
     "gqe_layer_forward": [_D, _LW, _P, _P, _P, _SZ, _P],
@@ -257,6 +266,81 @@ def gqe_attn_decode_noalloc(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, o_ro
 
 
 DECODE_NOALLOC_MAX_BYTES = 8 << 20
+
+
+# Sliding window with sinks, drafted trees (window 0: unlimited)
+
+def gqe_window_workspace_size(dims, op, L_max=0, window=0, sinks=0) -> int:
+    """Scratch bytes of the windowed and tree calls (may be 0)."""
+    n = _SZ(0)
+    _check("gqe_window_workspace_size", lib.gqe_window_workspace_size(
+        ctypes.byref(dims), op, int(L_max), int(window), int(sinks), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _scratch(ws):
+    """Pointer and size of a scratch tensor that may be absent."""
+    return (None, 0) if ws is None else (_ptr(ws, "ws"), ws.numel() * ws.element_size())
+
+
+def gqe_attn_prefill_window(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse=None, stream=None):
+    import torch
+    b = _bf16()
+    _check("gqe_attn_prefill_window", lib.gqe_attn_prefill_window(
+        ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True),
+        _ptr(K, "K", b), _ptr(V, "V", b), int(window), int(sinks), _ptr(o_routed, "o_routed", b),
+        _ptr(o_sh, "o_sh", b, optional=True), _ptr(lse, "lse", torch.float32, optional=True), _stream(stream)))
+
+
+def gqe_attn_prefill_window_bwd(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, do_routed, do_sh,
+                                dq_routed, dq_sh, dK, dV, ws, stream=None):
+    import torch
+    b = _bf16()
+    ws_bytes = ws.numel() * ws.element_size()
+    _check("gqe_attn_prefill_window_bwd", lib.gqe_attn_prefill_window_bwd(
+        ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True),
+        _ptr(K, "K", b), _ptr(V, "V", b), int(window), int(sinks), _ptr(o_routed, "o_routed", b),
+        _ptr(o_sh, "o_sh", b, optional=True), _ptr(lse, "lse", torch.float32), _ptr(do_routed, "do_routed", b),
+        _ptr(do_sh, "do_sh", b, optional=True), _ptr(dq_routed, "dq_routed", b),
+        _ptr(dq_sh, "dq_sh", b, optional=True), _ptr(dK, "dK", b), _ptr(dV, "dV", b), _ptr(ws, "ws"), ws_bytes,
+        _stream(stream)))
+
+
+def gqe_attn_decode_window(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, window, sinks, o_routed, o_sh, ws=None,
+                           stream=None):
+    import torch
+    b = _bf16()
+    wp, ws_bytes = _scratch(ws)
+    _check("gqe_attn_decode_window", lib.gqe_attn_decode_window(
+        ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True),
+        _ptr(Kc, "Kc", b), _ptr(Vc, "Vc", b), int(L_max), _ptr(cache_len, "cache_len", torch.int32), int(window),
+        int(sinks), _ptr(o_routed, "o_routed", b), _ptr(o_sh, "o_sh", b, optional=True), wp, ws_bytes,
+        _stream(stream)))
+
+
+def gqe_attn_tree(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max, cache_len, window, sinks, o_routed,
+                  o_sh, ws=None, stream=None):
+    """Attention of dims.T drafted tokens per sequence over the cache and over
+    their tree (parent [B, T] int32, tree_len [B] int32 or None)."""
+    import torch
+    b, i32 = _bf16(), torch.int32
+    wp, ws_bytes = _scratch(ws)
+    _check("gqe_attn_tree", lib.gqe_attn_tree(
+        ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True), _ptr(Kt, "Kt", b),
+        _ptr(Vt, "Vt", b), _ptr(parent, "parent", i32), _ptr(tree_len, "tree_len", i32, optional=True),
+        _ptr(Kc, "Kc", b), _ptr(Vc, "Vc", b), int(L_max), _ptr(cache_len, "cache_len", i32), int(window), int(sinks),
+        _ptr(o_routed, "o_routed", b), _ptr(o_sh, "o_sh", b, optional=True), wp, ws_bytes, _stream(stream)))
+
+
+def gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, L_max, cache_len, new_len, stream=None):
+    """Cache rows cache_len[b] .. += drafted rows path[b, :n_accept[b]];
+    new_len (may be cache_len) = cache_len + n_accept."""
+    import torch
+    b, i32 = _bf16(), torch.int32
+    _check("gqe_cache_commit", lib.gqe_cache_commit(
+        ctypes.byref(dims), _ptr(Kt, "Kt", b), _ptr(Vt, "Vt", b), _ptr(path, "path", i32),
+        _ptr(n_accept, "n_accept", i32), _ptr(Kc, "Kc", b), _ptr(Vc, "Vc", b), int(L_max),
+        _ptr(cache_len, "cache_len", i32), _ptr(new_len, "new_len", i32), _stream(stream)))
 
 
 def gqe_combine(dims, o_routed, o_sh, topk_w, h, stream=None):

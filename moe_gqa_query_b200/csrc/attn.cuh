@@ -14,6 +14,7 @@ struct AttnParams {
   int B, T, G, k, n_shared, sg;
   float scale_log2;       // scale * log2(e)
   unsigned* err;          // device error word
+  int window, sinks;      // windowed launches only: 1 <= window <= T, 0 <= sinks <= T
 };
 
 // diag.cu: a bounded wait that runs out (failure-path test)
@@ -22,6 +23,9 @@ cudaError_t launch_debug_wait(unsigned* err, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
                                 const CUtensorMap& mV, const AttnParams& p, int d,
                                 cudaStream_t stream);
+// The same attention under a sliding window with sinks (p.window, p.sinks).
+cudaError_t launch_attn_prefill_window(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
+                                       const CUtensorMap& mV, const AttnParams& p, int d, cudaStream_t stream);
 
 struct DecodeParams {
   const gqe_bf16_t* q_routed;   // [B, G, k, d]
@@ -62,6 +66,13 @@ struct AttnBwdParams {
   long long n_rows_pad;
   float scale, scale_log2;
   unsigned* err;
+  // windowed launches only: 1 <= window <= T, 0 <= sinks <= T, and the split of
+  // the sink tiles' walks
+  int window, sinks;
+  int sink_tiles;                   // key tiles that hold sinks and are split (0: none)
+  int split_len;                    // query tiles per part of a split walk
+  int n_parts;                      // parts per sink tile (the last ones may be empty)
+  float* part;                      // [sink_tiles, B*G, n_parts, 2 (dK, dV), 128, d] fp32
 };
 
 struct AttnBwdLayout {
@@ -70,10 +81,72 @@ struct AttnBwdLayout {
   size_t off_lse2, off_delta, off_dq, bytes;
 };
 
+// Windowed backward: how the sink tiles' long walks are split, and the scratch
+// (attn_bwd_layout's, then the parts).
+struct AttnBwdWindowPlan {
+  int sink_tiles, split_len, n_parts;
+  size_t off_part, bytes;
+};
+
+void attn_bwd_window_plan(int B, int T, int G, int k, int n_shared, int d, int window, int sinks,
+                          AttnBwdWindowPlan* P);
+cudaError_t launch_attn_bwd_window(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
+                                   const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
+                                   const CUtensorMap& mdQ, const AttnBwdParams& p, cudaStream_t stream);
+
 void attn_bwd_layout(int B, int T, int G, int k, int n_shared, int d, AttnBwdLayout* L);
 cudaError_t launch_attn_bwd(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
                             const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
                             const CUtensorMap& mdQ, const AttnBwdParams& p, cudaStream_t stream);
+
+// Attention of a few tokens per sequence against a dense cache (attn_cache.cu):
+// a tree of drafted tokens, or one new token under a window.
+constexpr int kMaxTree = 128;     // drafted tokens per sequence at most
+
+struct CacheAttnParams {
+  const gqe_bf16_t* q_routed;   // [B, G, T, k, d]
+  const gqe_bf16_t* q_sh;       // [B, T, d]
+  gqe_bf16_t* o_routed;
+  gqe_bf16_t* o_sh;
+  const int* cache_len;         // [B] cache rows of each sequence
+  const int* parent;            // [B, T] (tree)
+  const int* tree_len;          // [B] drafted tokens of each sequence, or null: T (tree)
+  float* part;                  // shares' states: O [items, rows_cap, d], then (m, l) [items, rows_cap, 2]
+  int B, T, G, k, n_shared, sg, L_max;
+  int tree;                     // 1: T drafted tokens behind the cache; 0: the cache's last row is the token itself
+  int window, sinks;            // window 0: unlimited
+  int n_qt, n_split, rows_cap;
+  float scale_log2;
+  unsigned* err;
+};
+
+struct CacheAttnPlan {
+  int n_qt, n_split, rows_cap;
+  long long items;              // CTAs: B * G * n_qt * n_split
+  size_t bytes;
+};
+
+void cache_attn_plan(int B, int T, int G, int k, int n_shared, int d, int L_max, bool tree, int window, int sinks,
+                     CacheAttnPlan* P);
+// Key rows per TMA box of the K and V maps.
+constexpr int cache_attn_key_tile(int d) { return d == 64 ? 128 : 64; }
+cudaError_t launch_attn_cache(const CUtensorMap& mK, const CUtensorMap& mV, const CUtensorMap& mKt,
+                              const CUtensorMap& mVt, const CacheAttnParams& p, int d, long long items,
+                              cudaStream_t stream);
+
+struct CommitParams {
+  const gqe_bf16_t* Kt;         // [B, G, T, d]
+  const gqe_bf16_t* Vt;
+  const int* path;              // [B, T]
+  const int* n_accept;          // [B]
+  gqe_bf16_t* Kc;               // [B, G, L_max, d]
+  gqe_bf16_t* Vc;
+  const int* cache_len;         // [B]
+  int* new_len;                 // [B], may be cache_len
+  int B, T, G, d, L_max;
+  unsigned* err;
+};
+cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t stream);
 
 size_t decode_workspace_bytes(int B, int G, int k, int d, int n_shared, int L_max);
 cudaError_t launch_attn_decode_maps(const CUtensorMap& mK, const CUtensorMap& mV, const DecodeParams& p,

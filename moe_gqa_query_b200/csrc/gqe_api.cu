@@ -421,10 +421,15 @@ gqe_status gqe_kv_append(const gqe_dims* dims, const gqe_bf16* x, const gqe_bf16
   return kv_common(dims, x, Wk, Wv, ep, dims->B, stream);
 }
 
-gqe_status gqe_attn_prefill(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
-                            const gqe_bf16* K, const gqe_bf16* V, gqe_bf16* o_routed, gqe_bf16* o_sh, float* lse,
-                            gqe_stream stream) {
+// Under a window of at least T tokens (or none, 0) attention is the full causal
+// one, and the kernels without a window run it.
+static bool has_window(const gqe_dims* dims, int window) { return window > 0 && window < dims->T; }
+
+static gqe_status prefill_common(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                 const gqe_bf16* K, const gqe_bf16* V, int window, int sinks, gqe_bf16* o_routed,
+                                 gqe_bf16* o_sh, float* lse, gqe_stream stream) {
   GQE_CHECK(check_dims(dims));
+  GQE_REQUIRE(window >= 0 && sinks >= 0, GQE_ERR_INVALID_ARG);
   GQE_REQUIRE(q_routed && K && V && o_routed, GQE_ERR_INVALID_ARG);
   GQE_REQUIRE(!dims->n_shared || (q_sh && o_sh), GQE_ERR_INVALID_ARG);
   GQE_REQUIRE(aligned16(q_routed) && aligned16(K) && aligned16(V) && aligned16(o_routed), GQE_ERR_INVALID_ARG);
@@ -448,15 +453,32 @@ gqe_status gqe_attn_prefill(const gqe_dims* dims, const gqe_bf16* q_routed, cons
   p.sg = dims->shared_kv_group;
   p.scale_log2 = scale_log2(dims);
   p.err = error_word();
-  return cuda_status(launch_attn_prefill(mQ, mQs, mK, mV, p, d, S(stream)));
+  if (!has_window(dims, window)) return cuda_status(launch_attn_prefill(mQ, mQs, mK, mV, p, d, S(stream)));
+  p.window = window;
+  p.sinks = sinks < T ? sinks : T;
+  return cuda_status(launch_attn_prefill_window(mQ, mQs, mK, mV, p, d, S(stream)));
 }
 
-gqe_status gqe_attn_prefill_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
-                                const gqe_bf16* K, const gqe_bf16* V, const gqe_bf16* o_routed,
-                                const gqe_bf16* o_sh, const float* lse, const gqe_bf16* do_routed,
-                                const gqe_bf16* do_sh, gqe_bf16* dq_routed, gqe_bf16* dq_sh, gqe_bf16* dK,
-                                gqe_bf16* dV, void* ws, size_t ws_bytes, gqe_stream stream) {
+gqe_status gqe_attn_prefill(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                            const gqe_bf16* K, const gqe_bf16* V, gqe_bf16* o_routed, gqe_bf16* o_sh, float* lse,
+                            gqe_stream stream) {
+  return prefill_common(dims, q_routed, q_sh, K, V, 0, 0, o_routed, o_sh, lse, stream);
+}
+
+gqe_status gqe_attn_prefill_window(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                   const gqe_bf16* K, const gqe_bf16* V, int window, int sinks, gqe_bf16* o_routed,
+                                   gqe_bf16* o_sh, float* lse, gqe_stream stream) {
+  return prefill_common(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, stream);
+}
+
+static gqe_status prefill_bwd_common(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                     const gqe_bf16* K, const gqe_bf16* V, int window, int sinks,
+                                     const gqe_bf16* o_routed, const gqe_bf16* o_sh, const float* lse,
+                                     const gqe_bf16* do_routed, const gqe_bf16* do_sh, gqe_bf16* dq_routed,
+                                     gqe_bf16* dq_sh, gqe_bf16* dK, gqe_bf16* dV, void* ws, size_t ws_bytes,
+                                     gqe_stream stream) {
   GQE_CHECK(check_dims(dims));
+  GQE_REQUIRE(window >= 0 && sinks >= 0, GQE_ERR_INVALID_ARG);
   GQE_REQUIRE(q_routed && K && V && o_routed && lse && do_routed && dq_routed && dK && dV, GQE_ERR_INVALID_ARG);
   GQE_REQUIRE(!dims->n_shared || (q_sh && o_sh && do_sh && dq_sh), GQE_ERR_INVALID_ARG);
   const void* ptrs[] = {q_routed, K, V, o_routed, do_routed, dq_routed, dK, dV, lse};
@@ -468,7 +490,12 @@ gqe_status gqe_attn_prefill_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, 
   const int B = dims->B, T = dims->T, G = dims->G, k = dims->k, d = dims->d_head;
   AttnBwdLayout L;
   attn_bwd_layout(B, T, G, k, dims->n_shared, d, &L);
-  GQE_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && ws_bytes >= L.bytes, GQE_ERR_WORKSPACE);
+  const bool win = has_window(dims, window);
+  const int n_sinks = sinks < T ? sinks : T;
+  AttnBwdWindowPlan P{};
+  P.bytes = L.bytes;
+  if (win) attn_bwd_window_plan(B, T, G, k, dims->n_shared, d, window, n_sinks, &P);
+  GQE_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && ws_bytes >= P.bytes, GQE_ERR_WORKSPACE);
   uint8_t* w = static_cast<uint8_t*>(ws);
   CUtensorMap mQ, mQs, mdO, mdOs, mK, mV, mdQ;
   GQE_REQUIRE(map3d(&mQ, q_routed, d, (uint64_t)T * k, (uint64_t)B * G, 128), GQE_ERR_CUDA);
@@ -510,8 +537,165 @@ gqe_status gqe_attn_prefill_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, 
   p.scale_log2 = scale_log2(dims);
   p.scale = p.scale_log2 / 1.4426950408889634f;
   p.err = error_word();
-  return cuda_status(launch_attn_bwd(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S(stream)));
+  if (!win) return cuda_status(launch_attn_bwd(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S(stream)));
+  p.window = window;
+  p.sinks = n_sinks;
+  // a window of one token without sinks: every softmax is over one key, whose
+  // weight is 1 whatever its score, so dS is 0 (and not the rounding that
+  // dP - Delta would leave)
+  if (window == 1 && n_sinks == 0) p.scale = 0.f;
+  p.sink_tiles = P.sink_tiles;
+  p.split_len = P.split_len;
+  p.n_parts = P.n_parts;
+  p.part = reinterpret_cast<float*>(w + P.off_part);
+  return cuda_status(launch_attn_bwd_window(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S(stream)));
 }
+
+gqe_status gqe_attn_prefill_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                const gqe_bf16* K, const gqe_bf16* V, const gqe_bf16* o_routed,
+                                const gqe_bf16* o_sh, const float* lse, const gqe_bf16* do_routed,
+                                const gqe_bf16* do_sh, gqe_bf16* dq_routed, gqe_bf16* dq_sh, gqe_bf16* dK,
+                                gqe_bf16* dV, void* ws, size_t ws_bytes, gqe_stream stream) {
+  return prefill_bwd_common(dims, q_routed, q_sh, K, V, 0, 0, o_routed, o_sh, lse, do_routed, do_sh, dq_routed, dq_sh,
+                            dK, dV, ws, ws_bytes, stream);
+}
+
+gqe_status gqe_attn_prefill_window_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                       const gqe_bf16* K, const gqe_bf16* V, int window, int sinks,
+                                       const gqe_bf16* o_routed, const gqe_bf16* o_sh, const float* lse,
+                                       const gqe_bf16* do_routed, const gqe_bf16* do_sh, gqe_bf16* dq_routed,
+                                       gqe_bf16* dq_sh, gqe_bf16* dK, gqe_bf16* dV, void* ws, size_t ws_bytes,
+                                       gqe_stream stream) {
+  return prefill_bwd_common(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, do_routed, do_sh,
+                            dq_routed, dq_sh, dK, dV, ws, ws_bytes, stream);
+}
+
+// Attention of dims->T query tokens per sequence over a cache: drafted tokens
+// (tree) or the cache's own last row (decode under a window).
+static gqe_status cache_attn_common(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                    const gqe_bf16* Kt, const gqe_bf16* Vt, const int32_t* parent,
+                                    const int32_t* tree_len, const gqe_bf16* Kc, const gqe_bf16* Vc, int L_max,
+                                    const int32_t* cache_len, int window, int sinks, bool tree, gqe_bf16* o_routed,
+                                    gqe_bf16* o_sh, void* ws, size_t ws_bytes, gqe_stream stream) {
+  GQE_CHECK(check_dims(dims));
+  GQE_REQUIRE(L_max >= 1 && window >= 0 && sinks >= 0, GQE_ERR_INVALID_ARG);
+  if (tree) GQE_REQUIRE(dims->T <= kMaxTree, GQE_ERR_UNSUPPORTED);
+  else GQE_REQUIRE(dims->T == 1, GQE_ERR_INVALID_ARG);
+  GQE_REQUIRE(q_routed && Kc && Vc && cache_len && o_routed, GQE_ERR_INVALID_ARG);
+  GQE_REQUIRE(!tree || (Kt && Vt && parent), GQE_ERR_INVALID_ARG);
+  GQE_REQUIRE(!dims->n_shared || (q_sh && o_sh), GQE_ERR_INVALID_ARG);
+  const void* ptrs[] = {q_routed, Kc, Vc, o_routed, tree ? Kt : Kc, tree ? Vt : Vc};
+  for (const void* q : ptrs) GQE_REQUIRE(aligned16(q), GQE_ERR_INVALID_ARG);
+  GQE_REQUIRE(!dims->n_shared || (aligned16(q_sh) && aligned16(o_sh)), GQE_ERR_INVALID_ARG);
+  const int B = dims->B, T = dims->T, G = dims->G, k = dims->k, d = dims->d_head;
+  CacheAttnPlan P;
+  cache_attn_plan(B, T, G, k, dims->n_shared, d, L_max, tree, window, sinks, &P);
+  GQE_REQUIRE(P.bytes == 0 || (ws && aligned16(ws) && ws_bytes >= P.bytes), GQE_ERR_WORKSPACE);
+  GQE_REQUIRE(P.items <= 0x7FFFFFFFll, GQE_ERR_UNSUPPORTED);
+  const uint32_t box = cache_attn_key_tile(d);
+  CUtensorMap mK, mV, mKt, mVt;
+  GQE_REQUIRE(map3d(&mK, Kc, d, L_max, (uint64_t)B * G, box), GQE_ERR_CUDA);
+  GQE_REQUIRE(map3d(&mV, Vc, d, L_max, (uint64_t)B * G, box), GQE_ERR_CUDA);
+  if (tree) {
+    GQE_REQUIRE(map3d(&mKt, Kt, d, T, (uint64_t)B * G, box), GQE_ERR_CUDA);
+    GQE_REQUIRE(map3d(&mVt, Vt, d, T, (uint64_t)B * G, box), GQE_ERR_CUDA);
+  } else {
+    mKt = mK;
+    mVt = mV;
+  }
+  CacheAttnParams p{};
+  p.q_routed = q_routed;
+  p.q_sh = q_sh;
+  p.o_routed = o_routed;
+  p.o_sh = o_sh;
+  p.cache_len = cache_len;
+  p.parent = parent;
+  p.tree_len = tree_len;
+  p.part = static_cast<float*>(ws);
+  p.B = B;
+  p.T = T;
+  p.G = G;
+  p.k = k;
+  p.n_shared = dims->n_shared;
+  p.sg = dims->shared_kv_group;
+  p.L_max = L_max;
+  p.tree = tree ? 1 : 0;
+  p.window = window;
+  p.sinks = sinks;
+  p.n_qt = P.n_qt;
+  p.n_split = P.n_split;
+  p.rows_cap = P.rows_cap;
+  p.scale_log2 = scale_log2(dims);
+  p.err = error_word();
+  return cuda_status(launch_attn_cache(mK, mV, mKt, mVt, p, d, P.items, S(stream)));
+}
+
+gqe_status gqe_attn_tree(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh, const gqe_bf16* Kt,
+                         const gqe_bf16* Vt, const int32_t* parent, const int32_t* tree_len, const gqe_bf16* Kc,
+                         const gqe_bf16* Vc, int L_max, const int32_t* cache_len, int window, int sinks,
+                         gqe_bf16* o_routed, gqe_bf16* o_sh, void* ws, size_t ws_bytes, gqe_stream stream) {
+  return cache_attn_common(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max, cache_len, window, sinks,
+                           true, o_routed, o_sh, ws, ws_bytes, stream);
+}
+
+gqe_status gqe_attn_decode_window(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
+                                  const gqe_bf16* Kc, const gqe_bf16* Vc, int L_max, const int32_t* cache_len,
+                                  int window, int sinks, gqe_bf16* o_routed, gqe_bf16* o_sh, void* ws,
+                                  size_t ws_bytes, gqe_stream stream) {
+  return cache_attn_common(dims, q_routed, q_sh, nullptr, nullptr, nullptr, nullptr, Kc, Vc, L_max, cache_len, window,
+                           sinks, false, o_routed, o_sh, ws, ws_bytes, stream);
+}
+
+gqe_status gqe_cache_commit(const gqe_dims* dims, const gqe_bf16* Kt, const gqe_bf16* Vt, const int32_t* path,
+                            const int32_t* n_accept, gqe_bf16* Kc, gqe_bf16* Vc, int L_max, const int32_t* cache_len,
+                            int32_t* new_len, gqe_stream stream) {
+  GQE_CHECK(check_dims(dims));
+  GQE_REQUIRE(L_max >= 1, GQE_ERR_INVALID_ARG);
+  GQE_REQUIRE(dims->T <= kMaxTree, GQE_ERR_UNSUPPORTED);
+  GQE_REQUIRE(Kt && Vt && path && n_accept && Kc && Vc && cache_len && new_len, GQE_ERR_INVALID_ARG);
+  GQE_REQUIRE(aligned16(Kt) && aligned16(Vt) && aligned16(Kc) && aligned16(Vc), GQE_ERR_INVALID_ARG);
+  CommitParams p{};
+  p.Kt = Kt;
+  p.Vt = Vt;
+  p.path = path;
+  p.n_accept = n_accept;
+  p.Kc = Kc;
+  p.Vc = Vc;
+  p.cache_len = cache_len;
+  p.new_len = new_len;
+  p.B = dims->B;
+  p.T = dims->T;
+  p.G = dims->G;
+  p.d = dims->d_head;
+  p.L_max = L_max;
+  p.err = error_word();
+  return cuda_status(launch_cache_commit(p, S(stream)));
+}
+
+gqe_status gqe_window_workspace_size(const gqe_dims* dims, int op, int L_max, int window, int sinks, size_t* bytes) {
+  GQE_CHECK(check_dims(dims));
+  GQE_REQUIRE(bytes && window >= 0 && sinks >= 0, GQE_ERR_INVALID_ARG);
+  const int B = dims->B, T = dims->T, G = dims->G, k = dims->k, d = dims->d_head;
+  if (op == GQE_OP_ATTN_WINDOW_BWD) {
+    if (!has_window(dims, window)) return gqe_workspace_size(dims, GQE_OP_ATTN_BWD, 0, bytes);
+    AttnBwdWindowPlan P;
+    attn_bwd_window_plan(B, T, G, k, dims->n_shared, d, window, sinks < T ? sinks : T, &P);
+    *bytes = P.bytes;
+    return GQE_OK;
+  }
+  if (op == GQE_OP_ATTN_DECODE_WINDOW || op == GQE_OP_ATTN_TREE) {
+    const bool tree = op == GQE_OP_ATTN_TREE;
+    GQE_REQUIRE(L_max >= 1, GQE_ERR_INVALID_ARG);
+    if (tree) GQE_REQUIRE(T <= kMaxTree, GQE_ERR_UNSUPPORTED);
+    else GQE_REQUIRE(T == 1, GQE_ERR_INVALID_ARG);
+    CacheAttnPlan P;
+    cache_attn_plan(B, T, G, k, dims->n_shared, d, L_max, tree, window, sinks, &P);
+    *bytes = P.bytes;
+    return GQE_OK;
+  }
+  return GQE_ERR_INVALID_ARG;
+}
+
 
 gqe_status gqe_attn_decode(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh, const gqe_bf16* Kc,
                            const gqe_bf16* Vc, int L_max, const int32_t* cache_len, gqe_bf16* o_routed,

@@ -20,6 +20,9 @@ enum DeviceErrorCode : unsigned {
   kErrTimeoutAttnBwd = 0x202,
   kErrTimeoutDecode = 0x301,
   kErrDecodeCacheLen = 0x302,  // a cache_len outside [1, L_max] (clamped; see gqe_attn_decode)
+  kErrTimeoutCacheAttn = 0x303,  // gqe_attn_tree, gqe_attn_decode_window
+  kErrTreeArgs = 0x304,        // a tree_len outside [0, T] or a parent outside [-1, i) (see gqe_attn_tree)
+  kErrCommitArgs = 0x305,      // gqe_cache_commit: a count, length or path entry outside its range
   kErrTimeoutRouter = 0x401,
   kErrTimeoutDebug = 0x7F1,   // gqe_debug_wait_timeout: a wait that nothing completes
 };

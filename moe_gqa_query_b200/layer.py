@@ -8,8 +8,13 @@ stream; every step of the forward runs in libgqe.so's kernels:
            projection, without materialising h where the shape allows)
   decode   gqe_router_topk -> gqe_routed_qproj -> gqe_kv_append ->
            gqe_attn_decode -> gqe_combine -> gqe_linear
+  drafts   gqe_router_topk -> gqe_routed_qproj -> gqe_kv_proj ->
+           gqe_attn_tree -> gqe_combine_out_proj, then gqe_cache_commit
   backward gqe_gemm (dh, dWo) -> gqe_combine_bwd -> gqe_attn_prefill_bwd ->
            gqe_router_bwd -> gqe_bwd_pack -> gqe_gemm (dx, dW_cat)
+
+With GQEConfig.window set, every attention call is its windowed form: a token
+sees the last `window` tokens up to itself and the first `sinks` tokens.
 
 Weight layouts (bf16): Wr [D, G*E]; Wq [G, E, d, D]; Wk, Wv [G*d, D];
 Wsh [n_shared*d, D]; Wo [D, slots*d] with slots = k*G + 1 + n_shared (GQE's
@@ -38,6 +43,12 @@ class GQEConfig:
     renorm_scope: int = 0
     scale: float = 0.0
     output_mode: int = 0
+    window: int = 0         # tokens a token sees, itself included (0: all before it)
+    sinks: int = 0          # first tokens that stay visible behind the window
+
+    def __post_init__(self):
+        if self.window < 0 or self.sinks < 0:
+            raise ValueError(f"window {self.window} and sinks {self.sinks} must not be negative")
 
     @property
     def slots(self) -> int:
@@ -138,7 +149,10 @@ class GQELayer:
             L.gqe_router_topk(dims, x, self.Wr, self.bias, idx, w, probs, stream)
             L.gqe_routed_qproj(dims, x, self.Wq, self.Wsh, idx, q, qs, ws, None, stream)
             L.gqe_kv_proj(dims, x, self.Wk, self.Wv, K, V, stream)
-        L.gqe_attn_prefill(dims, q, qs, K, V, o, os_, lse, stream)
+        if c.window:
+            L.gqe_attn_prefill_window(dims, q, qs, K, V, c.window, c.sinks, o, os_, lse, stream)
+        else:
+            L.gqe_attn_prefill(dims, q, qs, K, V, o, os_, lse, stream)
         L.gqe_combine_out_proj(dims, o, os_, w, self.Wo, y, ws_o, stream)
         if keep:
             h = self._buf("h", (N, c.slots * c.d))
@@ -183,9 +197,14 @@ class GQELayer:
         dq_sh = buf("dq_sh", (B, T, d)) if c.n_shared else None
         dK = buf("dK", (B, c.G, T, d))
         dV = buf("dV", (B, c.G, T, d))
-        ws_a = self._ws("ws_a", L.gqe_workspace_size(dims, L.GQE_OP_ATTN_BWD))
-        L.gqe_attn_prefill_bwd(dims, saved["q"], saved["q_sh"], saved["K"], saved["V"], saved["o"], saved["o_sh"],
-                               saved["lse"], do, do_sh, dq, dq_sh, dK, dV, ws_a, stream)
+        fwd = (saved["q"], saved["q_sh"], saved["K"], saved["V"])
+        rest = (saved["o"], saved["o_sh"], saved["lse"], do, do_sh, dq, dq_sh, dK, dV)
+        if c.window:
+            ws_a = self._ws("ws_a", L.gqe_window_workspace_size(dims, L.GQE_OP_ATTN_WINDOW_BWD, 0, c.window, c.sinks))
+            L.gqe_attn_prefill_window_bwd(dims, *fwd, c.window, c.sinks, *rest, ws_a, stream)
+        else:
+            ws_a = self._ws("ws_a", L.gqe_workspace_size(dims, L.GQE_OP_ATTN_BWD))
+            L.gqe_attn_prefill_bwd(dims, *fwd, *rest, ws_a, stream)
         dlogits = buf("dlogits", (N, GE), torch.float32)
         dbias = buf("dbias", (GE,), torch.float32)
         L.gqe_router_bwd(dims, saved["probs"], saved["idx"], saved["w"], dw, dlogits, dbias, stream)
@@ -247,6 +266,9 @@ class GQELayer:
         layer's streams, each call's copies overlapping the previous call's
         last steps; join once after the last one."""
         c = self.cfg
+        if c.window:
+            raise ValueError("gqe_layer_forward_host runs full causal attention; a windowed layer has forward, "
+                             "forward_graph, forward_host and forward_host_pipelined")
         B, T = x_host.shape[0], x_host.shape[1]
         chunk = max(1, int(chunk_seqs))
         # the scratch's layout depends on T and chunk_seqs alone, so batches of
@@ -339,13 +361,71 @@ class GQELayer:
         h = self._buf("d_h", (B, c.slots * c.d))
         y = self._buf("d_y", (B, c.D))
         wsq = self._ws("d_ws_q", L.gqe_workspace_size(dims, L.GQE_OP_ROUTED_QPROJ))
-        wsd = self._ws("d_ws_a", L.gqe_workspace_size(dims, L.GQE_OP_ATTN_DECODE, L_max))
+        if c.window:
+            nws = L.gqe_window_workspace_size(dims, L.GQE_OP_ATTN_DECODE_WINDOW, L_max, c.window, c.sinks)
+        else:
+            nws = L.gqe_workspace_size(dims, L.GQE_OP_ATTN_DECODE, L_max)
+        wsd = self._ws("d_ws_a", nws)
         L.gqe_router_topk(dims, x_new, self.Wr, self.bias, idx, w, None, stream)
         L.gqe_routed_qproj(dims, x_new, self.Wq, self.Wsh, idx, q, qs, wsq, None, stream)
         L.gqe_kv_append(dims, x_new, self.Wk, self.Wv, Kc, Vc, L_max, cache_len, stream)
-        L.gqe_attn_decode(dims, q, qs, Kc, Vc, L_max, cache_len, o, os_, wsd, stream)
+        if c.window:
+            L.gqe_attn_decode_window(dims, q, qs, Kc, Vc, L_max, cache_len, c.window, c.sinks, o, os_, wsd, stream)
+        else:
+            L.gqe_attn_decode(dims, q, qs, Kc, Vc, L_max, cache_len, o, os_, wsd, stream)
         L.gqe_combine(dims, o, os_, w, h, stream)
         L.gqe_linear(h, self.Wo, y, stream)
         if keep:
             return y, dict(idx=idx, w=w, q=q, q_sh=qs, o=o, o_sh=os_, h=h)
         return y
+
+    # ------------------------------------------------------------------ drafted tokens
+    def decode_tree(self, x_draft: torch.Tensor, parent: torch.Tensor, Kc: torch.Tensor, Vc: torch.Tensor,
+                    cache_len: torch.Tensor, tree_len=None, stream=None, keep=False):
+        """A tree of drafted tokens per sequence in one step (speculative
+        decoding).  x_draft [B, T, D], T <= 128; parent [B, T] int32 (-1: the
+        token follows the cache's last row, else an earlier drafted token);
+        tree_len [B] int32 or None (T everywhere); cache_len [B] int32 rows in
+        the cache Kc, Vc [B, G, L_max, d], the drafted tokens not included.
+
+        Returns y [B, T, D] and the draft (its K and V rows) for commit().
+        Both are the layer's own buffers, overwritten by the next decode_tree;
+        rows past tree_len of y hold nothing of use.  The cache is read only."""
+        c = self.cfg
+        B, T = x_draft.shape[0], x_draft.shape[1]
+        L_max = Kc.shape[2]
+        dims = L.make_dims(c, B=B, T=T)
+        N = B * T
+        idx = self._buf("t_idx", (N, c.G, c.k), torch.int32)
+        w = self._buf("t_w", (N, c.G, c.k), torch.float32)
+        q = self._buf("t_q", (B, c.G, T, c.k, c.d))
+        qs = self._buf("t_qs", (B, T, c.d)) if c.n_shared else None
+        Kt = self._buf("t_K", (B, c.G, T, c.d))
+        Vt = self._buf("t_V", (B, c.G, T, c.d))
+        o = self._buf("t_o", (B, c.G, T, c.k, c.d))
+        os_ = self._buf("t_os", (B, T, c.d)) if c.n_shared else None
+        y = self._buf("t_y", (B, T, c.D))
+        wsq = self._ws("t_ws_q", L.gqe_workspace_size(dims, L.GQE_OP_ROUTED_QPROJ))
+        wsa = self._ws("t_ws_a", L.gqe_window_workspace_size(dims, L.GQE_OP_ATTN_TREE, L_max, c.window, c.sinks))
+        wso = self._ws("t_ws_o", L.gqe_workspace_size(dims, L.GQE_OP_COMBINE_OUT_PROJ))
+        L.gqe_router_topk(dims, x_draft, self.Wr, self.bias, idx, w, None, stream)
+        L.gqe_routed_qproj(dims, x_draft, self.Wq, self.Wsh, idx, q, qs, wsq, None, stream)
+        L.gqe_kv_proj(dims, x_draft, self.Wk, self.Wv, Kt, Vt, stream)
+        L.gqe_attn_tree(dims, q, qs, Kt, Vt, parent, tree_len, Kc, Vc, L_max, cache_len, c.window, c.sinks, o, os_,
+                        wsa, stream)
+        L.gqe_combine_out_proj(dims, o, os_, w, self.Wo, y, wso, stream)
+        draft = dict(K=Kt, V=Vt)
+        if keep:
+            draft.update(idx=idx, w=w, q=q, q_sh=qs, o=o, o_sh=os_)
+        return y, draft
+
+    def commit(self, draft: dict, path: torch.Tensor, n_accept: torch.Tensor, Kc: torch.Tensor, Vc: torch.Tensor,
+               cache_len: torch.Tensor, new_len=None, stream=None) -> torch.Tensor:
+        """Moves the accepted drafted tokens of a decode_tree to the end of the
+        cache: path [B, T] int32 (drafted tokens in order), n_accept [B] int32.
+        The new lengths go to new_len, or into cache_len itself without one."""
+        Kt, Vt = draft["K"], draft["V"]
+        dims = L.make_dims(self.cfg, B=Kt.shape[0], T=Kt.shape[2])
+        new_len = cache_len if new_len is None else new_len
+        L.gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, Kc.shape[2], cache_len, new_len, stream)
+        return new_len
