@@ -13,6 +13,8 @@ import ctypes
 import os
 import re
 
+import torch
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # GQE_LIB_PATH selects another build of the library (the traced diagnostic
 # build, libgqe_trace.so); by default the package's own libgqe.so.
@@ -148,10 +150,16 @@ def _ptr(t, name="tensor", dtype=None, optional=False):
     return t.data_ptr()
 
 
+# The current stream's handle.  torch.cuda.current_stream() builds a Stream
+# object for it: 3.5 us of a call's host time, the raw handle 0.3 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -163,7 +171,6 @@ def _check(fn, st):
 
 
 def _bf16():
-    import torch
     return torch.bfloat16
 
 
@@ -177,7 +184,6 @@ def gqe_workspace_size(dims: gqe_dims, op: int, L_max: int = 0) -> int:
 
 
 def gqe_router_topk(dims, x, Wr, bias, topk_idx, topk_w, probs=None, stream=None):
-    import torch
     _check("gqe_router_topk", lib.gqe_router_topk(
         ctypes.byref(dims), _ptr(x, "x", _bf16()), _ptr(Wr, "Wr", _bf16()),
         _ptr(bias, "bias", torch.float32, optional=True), _ptr(topk_idx, "topk_idx", torch.int32),
@@ -186,14 +192,12 @@ def gqe_router_topk(dims, x, Wr, bias, topk_idx, topk_w, probs=None, stream=None
 
 
 def gqe_router_stats(dims, probs, topk_idx, counts, prob_sum, stream=None):
-    import torch
     _check("gqe_router_stats", lib.gqe_router_stats(
         ctypes.byref(dims), _ptr(probs, "probs", torch.float32), _ptr(topk_idx, "topk_idx", torch.int32),
         _ptr(counts, "counts", torch.int32), _ptr(prob_sum, "prob_sum", torch.float32), _stream(stream)))
 
 
 def gqe_routed_qproj(dims, x, Wq, Wsh, topk_idx, q_routed, q_sh, ws, expert_counts=None, stream=None):
-    import torch
     ws_bytes = ws.numel() * ws.element_size()
     _check("gqe_routed_qproj", lib.gqe_routed_qproj(
         ctypes.byref(dims), _ptr(x, "x", _bf16()), _ptr(Wq, "Wq", _bf16()),
@@ -211,7 +215,6 @@ def gqe_kv_proj(dims, x, Wk, Wv, K, V, stream=None):
 
 
 def gqe_kv_append(dims, x, Wk, Wv, Kc, Vc, L_max, cache_len, stream=None):
-    import torch
     b = _bf16()
     _check("gqe_kv_append", lib.gqe_kv_append(
         ctypes.byref(dims), _ptr(x, "x", b), _ptr(Wk, "Wk", b), _ptr(Wv, "Wv", b),
@@ -220,7 +223,6 @@ def gqe_kv_append(dims, x, Wk, Wv, Kc, Vc, L_max, cache_len, stream=None):
 
 
 def gqe_attn_prefill(dims, q_routed, q_sh, K, V, o_routed, o_sh, lse=None, stream=None):
-    import torch
     b = _bf16()
     _check("gqe_attn_prefill", lib.gqe_attn_prefill(
         ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True),
@@ -231,7 +233,6 @@ def gqe_attn_prefill(dims, q_routed, q_sh, K, V, o_routed, o_sh, lse=None, strea
 
 def gqe_attn_prefill_bwd(dims, q_routed, q_sh, K, V, o_routed, o_sh, lse, do_routed, do_sh,
                          dq_routed, dq_sh, dK, dV, ws, stream=None):
-    import torch
     b = _bf16()
     ws_bytes = ws.numel() * ws.element_size()
     _check("gqe_attn_prefill_bwd", lib.gqe_attn_prefill_bwd(
@@ -243,7 +244,6 @@ def gqe_attn_prefill_bwd(dims, q_routed, q_sh, K, V, o_routed, o_sh, lse, do_rou
 
 
 def gqe_attn_decode(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, o_routed, o_sh, ws, stream=None):
-    import torch
     b = _bf16()
     ws_bytes = ws.numel() * ws.element_size()
     _check("gqe_attn_decode", lib.gqe_attn_decode(
@@ -257,7 +257,6 @@ def gqe_attn_decode_noalloc(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, o_ro
     """gqe_attn_decode with the partial states in the library's fixed device
     array instead of a caller workspace: for callers that cannot allocate
     device memory at decode time.  Calls must not overlap on the GPU."""
-    import torch
     b = _bf16()
     _check("gqe_attn_decode_noalloc", lib.gqe_attn_decode_noalloc(
         ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True),
@@ -278,43 +277,57 @@ def gqe_window_workspace_size(dims, op, L_max=0, window=0, sinks=0) -> int:
     return int(n.value)
 
 
-def _scratch(ws):
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
+def _dev(t, name, dtype, dev, optional=False):
+    """_ptr for the calls below, which also refuse a tensor of another device
+    than the current one, dev (the library launches on the current device)."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        return _ptr(t, name)
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _ptr(t, name, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return t.data_ptr()
+
+
+def _scratch(ws, dev):
     """Pointer and size of a scratch tensor that may be absent."""
-    return (None, 0) if ws is None else (_ptr(ws, "ws"), ws.numel() * ws.element_size())
+    return (None, 0) if ws is None else (_dev(ws, "ws", ws.dtype, dev), ws.numel() * ws.element_size())
 
 
 def gqe_attn_prefill_window(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse=None, stream=None):
-    import torch
-    b = _bf16()
+    dev = torch.cuda.current_device()
     _check("gqe_attn_prefill_window", lib.gqe_attn_prefill_window(
-        ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True),
-        _ptr(K, "K", b), _ptr(V, "V", b), int(window), int(sinks), _ptr(o_routed, "o_routed", b),
-        _ptr(o_sh, "o_sh", b, optional=True), _ptr(lse, "lse", torch.float32, optional=True), _stream(stream)))
+        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
+        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), int(window), int(sinks), _dev(o_routed, "o_routed", _BF16, dev),
+        _dev(o_sh, "o_sh", _BF16, dev, True), _dev(lse, "lse", _F32, dev, True), _stream(stream)))
 
 
 def gqe_attn_prefill_window_bwd(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, do_routed, do_sh,
                                 dq_routed, dq_sh, dK, dV, ws, stream=None):
-    import torch
-    b = _bf16()
-    ws_bytes = ws.numel() * ws.element_size()
+    dev = torch.cuda.current_device()
+    wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_prefill_window_bwd", lib.gqe_attn_prefill_window_bwd(
-        ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True),
-        _ptr(K, "K", b), _ptr(V, "V", b), int(window), int(sinks), _ptr(o_routed, "o_routed", b),
-        _ptr(o_sh, "o_sh", b, optional=True), _ptr(lse, "lse", torch.float32), _ptr(do_routed, "do_routed", b),
-        _ptr(do_sh, "do_sh", b, optional=True), _ptr(dq_routed, "dq_routed", b),
-        _ptr(dq_sh, "dq_sh", b, optional=True), _ptr(dK, "dK", b), _ptr(dV, "dV", b), _ptr(ws, "ws"), ws_bytes,
+        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
+        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), int(window), int(sinks), _dev(o_routed, "o_routed", _BF16, dev),
+        _dev(o_sh, "o_sh", _BF16, dev, True), _dev(lse, "lse", _F32, dev), _dev(do_routed, "do_routed", _BF16, dev),
+        _dev(do_sh, "do_sh", _BF16, dev, True), _dev(dq_routed, "dq_routed", _BF16, dev),
+        _dev(dq_sh, "dq_sh", _BF16, dev, True), _dev(dK, "dK", _BF16, dev), _dev(dV, "dV", _BF16, dev), wp, ws_bytes,
         _stream(stream)))
 
 
 def gqe_attn_decode_window(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, window, sinks, o_routed, o_sh, ws=None,
                            stream=None):
-    import torch
-    b = _bf16()
-    wp, ws_bytes = _scratch(ws)
+    dev = torch.cuda.current_device()
+    wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_decode_window", lib.gqe_attn_decode_window(
-        ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True),
-        _ptr(Kc, "Kc", b), _ptr(Vc, "Vc", b), int(L_max), _ptr(cache_len, "cache_len", torch.int32), int(window),
-        int(sinks), _ptr(o_routed, "o_routed", b), _ptr(o_sh, "o_sh", b, optional=True), wp, ws_bytes,
+        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
+        _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max), _dev(cache_len, "cache_len", _I32, dev), int(window),
+        int(sinks), _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes,
         _stream(stream)))
 
 
@@ -322,29 +335,26 @@ def gqe_attn_tree(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max,
                   o_sh, ws=None, stream=None):
     """Attention of dims.T drafted tokens per sequence over the cache and over
     their tree (parent [B, T] int32, tree_len [B] int32 or None)."""
-    import torch
-    b, i32 = _bf16(), torch.int32
-    wp, ws_bytes = _scratch(ws)
+    dev = torch.cuda.current_device()
+    wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_tree", lib.gqe_attn_tree(
-        ctypes.byref(dims), _ptr(q_routed, "q_routed", b), _ptr(q_sh, "q_sh", b, optional=True), _ptr(Kt, "Kt", b),
-        _ptr(Vt, "Vt", b), _ptr(parent, "parent", i32), _ptr(tree_len, "tree_len", i32, optional=True),
-        _ptr(Kc, "Kc", b), _ptr(Vc, "Vc", b), int(L_max), _ptr(cache_len, "cache_len", i32), int(window), int(sinks),
-        _ptr(o_routed, "o_routed", b), _ptr(o_sh, "o_sh", b, optional=True), wp, ws_bytes, _stream(stream)))
+        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True), _dev(Kt, "Kt", _BF16, dev),
+        _dev(Vt, "Vt", _BF16, dev), _dev(parent, "parent", _I32, dev), _dev(tree_len, "tree_len", _I32, dev, True),
+        _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max), _dev(cache_len, "cache_len", _I32, dev), int(window), int(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes, _stream(stream)))
 
 
 def gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, L_max, cache_len, new_len, stream=None):
     """Cache rows cache_len[b] .. += drafted rows path[b, :n_accept[b]];
     new_len (may be cache_len) = cache_len + n_accept."""
-    import torch
-    b, i32 = _bf16(), torch.int32
+    dev = torch.cuda.current_device()
     _check("gqe_cache_commit", lib.gqe_cache_commit(
-        ctypes.byref(dims), _ptr(Kt, "Kt", b), _ptr(Vt, "Vt", b), _ptr(path, "path", i32),
-        _ptr(n_accept, "n_accept", i32), _ptr(Kc, "Kc", b), _ptr(Vc, "Vc", b), int(L_max),
-        _ptr(cache_len, "cache_len", i32), _ptr(new_len, "new_len", i32), _stream(stream)))
+        ctypes.byref(dims), _dev(Kt, "Kt", _BF16, dev), _dev(Vt, "Vt", _BF16, dev), _dev(path, "path", _I32, dev),
+        _dev(n_accept, "n_accept", _I32, dev), _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max),
+        _dev(cache_len, "cache_len", _I32, dev), _dev(new_len, "new_len", _I32, dev), _stream(stream)))
 
 
 def gqe_combine(dims, o_routed, o_sh, topk_w, h, stream=None):
-    import torch
     b = _bf16()
     _check("gqe_combine", lib.gqe_combine(
         ctypes.byref(dims), _ptr(o_routed, "o_routed", b), _ptr(o_sh, "o_sh", b, optional=True),
@@ -352,7 +362,6 @@ def gqe_combine(dims, o_routed, o_sh, topk_w, h, stream=None):
 
 
 def gqe_combine_out_proj(dims, o_routed, o_sh, topk_w, Wo, y, ws, stream=None):
-    import torch
     b = _bf16()
     ws_bytes = ws.numel() * ws.element_size()
     _check("gqe_combine_out_proj", lib.gqe_combine_out_proj(
@@ -366,7 +375,6 @@ def layer_weights(src) -> gqe_layer_weights:
     GQELayer) or dict holding the device tensors Wr, bias, Wq, Wsh, Wk, Wv, Wo
     (bias and Wsh may be None).  The struct holds raw pointers: keep the
     tensors alive while it is in use."""
-    import torch
     get = src.get if isinstance(src, dict) else (lambda k: getattr(src, k, None))
     b = _bf16()
     return gqe_layer_weights(
@@ -433,7 +441,6 @@ def gqe_gemm(A, a_kn, B, b_kn, C, stream=None):
 
 def gqe_gemm_acc(A, a_kn, B, b_kn, C, accumulate=False, stream=None):
     """C [M, N] fp32 = (C if accumulate else 0) + A B^T over K (layouts as gqe_gemm)."""
-    import torch
     b = _bf16()
     A2 = A.reshape(-1, A.shape[-1])
     B2 = B.reshape(-1, B.shape[-1])
@@ -448,7 +455,6 @@ def gqe_gemm_acc(A, a_kn, B, b_kn, C, accumulate=False, stream=None):
 
 
 def gqe_combine_bwd(dims, o_routed, o_sh, topk_w, dh, do_routed, do_sh, dtopk_w, stream=None):
-    import torch
     b = _bf16()
     _check("gqe_combine_bwd", lib.gqe_combine_bwd(
         ctypes.byref(dims), _ptr(o_routed, "o_routed", b), _ptr(o_sh, "o_sh", b, optional=True),
@@ -457,7 +463,6 @@ def gqe_combine_bwd(dims, o_routed, o_sh, topk_w, dh, do_routed, do_sh, dtopk_w,
 
 
 def gqe_router_bwd(dims, probs, topk_idx, topk_w, dtopk_w, dlogits, dbias=None, stream=None):
-    import torch
     f = torch.float32
     _check("gqe_router_bwd", lib.gqe_router_bwd(
         ctypes.byref(dims), _ptr(probs, "probs", f), _ptr(topk_idx, "topk_idx", torch.int32),
@@ -472,7 +477,6 @@ def gqe_bwd_pack_cols(dims) -> int:
 
 
 def gqe_bwd_pack(dims, topk_idx, dq_routed, dq_sh, dK, dV, dlogits, A, stream=None):
-    import torch
     b = _bf16()
     _check("gqe_bwd_pack", lib.gqe_bwd_pack(
         ctypes.byref(dims), _ptr(topk_idx, "topk_idx", torch.int32), _ptr(dq_routed, "dq_routed", b),
@@ -498,7 +502,6 @@ def gqe_transpose(src, dst, ld_dst=None, stream=None):
 
 def gqe_transpose_f32(src, dst, ld_dst=None, stream=None):
     """dst [cols, ld_dst] <- src [rows, cols]^T, fp32."""
-    import torch
     rows, cols = src.shape[0], src.numel() // src.shape[0]
     ld = rows if ld_dst is None else int(ld_dst)
     _check("gqe_transpose_f32", lib.gqe_transpose_f32(rows, cols, _ptr(src, "src", torch.float32),
@@ -516,7 +519,6 @@ def gqe_debug_wait_timeout(stream=None):
 
 
 def gqe_debug_exp2(x, y_poly, y_pair, y_hw, stream=None):
-    import torch
     f = torch.float32
     _check("gqe_debug_exp2", lib.gqe_debug_exp2(_ptr(x, "x", f), _ptr(y_poly, "y_poly", f), _ptr(y_pair, "y_pair", f),
                                                 _ptr(y_hw, "y_hw", f), x.numel(), _stream(stream)))

@@ -111,19 +111,17 @@ struct CacheAttnParams {
   const int* cache_len;         // [B] cache rows of each sequence
   const int* parent;            // [B, T] (tree)
   const int* tree_len;          // [B] drafted tokens of each sequence, or null: T (tree)
-  float* part;                  // shares' states: O [items, rows_cap, d], then (m, l) [items, rows_cap, 2]
   int B, T, G, k, n_shared, sg, L_max;
   int tree;                     // 1: T drafted tokens behind the cache; 0: the cache's last row is the token itself
   int window, sinks;            // window 0: unlimited
-  int n_qt, n_split, rows_cap;
+  int n_qt, n_split;            // query tiles per (b, g); shares (CTAs of a cluster) per query tile
   float scale_log2;
   unsigned* err;
 };
 
 struct CacheAttnPlan {
-  int n_qt, n_split, rows_cap;
+  int n_qt, n_split;
   long long items;              // CTAs: B * G * n_qt * n_split
-  size_t bytes;
 };
 
 void cache_attn_plan(int B, int T, int G, int k, int n_shared, int d, int L_max, bool tree, int window, int sinks,

@@ -12,8 +12,10 @@
 // The T*k routed rows of a group, and the shared head's T rows when the group
 // is the shared head's, are packed into 128-row query tiles, so each key tile
 // is read once for all of them.  Work item: one query tile of one (b, g) and a
-// share of its key list; the shares' softmax states (max, sum, unnormalised O,
-// fp32) are joined by attn_cache_merge_kernel.
+// share of its key list.  The CTAs of one query tile's shares form a cluster:
+// each leaves its rows' softmax state (max, sum, unnormalised O, fp32) in its
+// own shared memory, and after a cluster barrier the CTAs divide the rows among
+// them and join the states over distributed shared memory.
 //
 // Per CTA (192 threads, two CTAs per SM): warp 4 brings K tiles by TMA and
 // issues S = Q K^T, warp 5 brings V tiles and issues O += P V (P from tensor
@@ -39,13 +41,14 @@ namespace {
 
 constexpr int kRowsQ = 128;       // query rows per tile
 constexpr int kCacheThreads = 192;
-constexpr int kCacheST = 2;       // K/V ring depth
 constexpr float kCacheRescaleLog2 = 8.0f;
 
 template <int D>
 struct CacheCfg {
   static constexpr int NB = D / 64;
   static constexpr int KT = D == 64 ? 128 : 64;          // keys per tile
+  static constexpr int KST = D == 64 ? 3 : 2;            // K and V ring depths
+  static constexpr int VST = 2;
   static constexpr int QBox = kRowsQ * 128;              // 128 rows x 64 bf16
   static constexpr int KBox = KT * 128;
   static constexpr int QBytes = NB * QBox;
@@ -55,11 +58,12 @@ struct CacheCfg {
 };
 
 struct __align__(16) CacheShared {
-  uint32_t anc[2][kMaxTree][4];      // ancestor bits (double-buffered while they are built)
+  uint4 anc[2][kMaxTree];            // ancestor bits (double-buffered while they are built)
   int up[2][kMaxTree];               // pointer doubling: 2^r levels up, -1 past the root
   int depth[2][kMaxTree];
-  float m[kRowsQ], l[kRowsQ];
-  uint64_t k_full[kCacheST], k_empty[kCacheST], v_full[kCacheST], v_empty[kCacheST];
+  float m[kRowsQ], l[kRowsQ];        // per lane
+  float row_m[kRowsQ], row_l[kRowsQ];   // per row, its repeats joined
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t s_full, s_free, p_full, pv_done;
   uint32_t tmem_base;
   int abort;
@@ -67,7 +71,7 @@ struct __align__(16) CacheShared {
 
 template <int D>
 constexpr size_t cache_smem() {
-  return 1024 + CacheCfg<D>::QBytes + 2 * kCacheST * CacheCfg<D>::KVBytes + sizeof(CacheShared);
+  return 1024 + CacheCfg<D>::QBytes + (CacheCfg<D>::KST + CacheCfg<D>::VST) * CacheCfg<D>::KVBytes + sizeof(CacheShared);
 }
 
 // One sequence's keys as this query tile's list of key tiles.
@@ -229,10 +233,10 @@ __device__ __forceinline__ RowState cache_softmax(const CacheAttnParams& p, cons
     const bool dead_keys = in_tree ? kb + KT > cl.m
                                    : kb + KT > cl.len || (p.window && kb < cl.lo0 && kb + KT > p.sinks);
     if (dead_keys) {
-      st.ok = mbar_wait(&sh->v_full[j % kCacheST], (j / kCacheST) & 1, abort, p.err, kErrTimeoutCacheAttn) && st.ok;
+      st.ok = mbar_wait(&sh->v_full[j % C::VST], (j / C::VST) & 1, abort, p.err, kErrTimeoutCacheAttn) && st.ok;
       const int r = threadIdx.x, pos = kb + r;
       if (r < KT && (in_tree ? pos >= cl.m : pos >= cl.len || (pos < cl.lo0 && pos >= p.sinks))) {
-        uint8_t* row = sV + (j % kCacheST) * C::KVBytes + r * 128;
+        uint8_t* row = sV + (j % C::VST) * C::KVBytes + r * 128;
 #pragma unroll
         for (int bx = 0; bx < C::NB; ++bx)
 #pragma unroll
@@ -258,19 +262,150 @@ __device__ __forceinline__ T* row_ptr(T* routed, T* shared, const CacheAttnParam
                  : shared + ((size_t)(bg / p.G) * p.T + t) * D;
 }
 
+// Ancestor bits and depths of the drafted tokens by pointer doubling, on the
+// 128 threads of the softmax warps: after round r a token's bits cover
+// 2^(r+1) - 1 levels above it.  up: thread i's parent[i].  Returns the buffer
+// that holds the result.
+__device__ __forceinline__ int build_tree(const CacheAttnParams& p, const CacheList& cl, CacheShared* sh, int up) {
+  const int i = threadIdx.x;
+  if (up < -1 || up >= i) {
+    if (p.err) atomicCAS(p.err, 0u, (unsigned)kErrTreeArgs);
+    up = -1;
+  }
+  uint32_t own[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    own[w] = ((i >> 5) == w ? 1u << (i & 31) : 0u) | (up >= 0 && (up >> 5) == w ? 1u << (up & 31) : 0u);
+  uint4 anc = make_uint4(own[0], own[1], own[2], own[3]);
+  int depth = up >= 0 ? 1 : 0, cur = 0;
+  for (int span = 1; span < p.T; span *= 2) {
+    if (i < p.T) {
+      sh->anc[cur][i] = anc;
+      sh->depth[cur][i] = depth;
+      sh->up[cur][i] = up;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (up >= 0) {
+      const uint4 a = sh->anc[cur][up];
+      anc.x |= a.x, anc.y |= a.y, anc.z |= a.z, anc.w |= a.w;
+      depth += sh->depth[cur][up];
+      up = sh->up[cur][up];
+    }
+    cur ^= 1;
+  }
+  if (i < p.T) {
+    sh->anc[cur][i] = anc;
+    sh->depth[cur][i] = depth;
+  }
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  if (p.window && p.window < p.T && i < p.T) {
+    // ancestors that the window has left behind
+    uint32_t* bits = reinterpret_cast<uint32_t*>(&sh->anc[cur][i]);
+    for (int a = 0; a < i; ++a)
+      if (depth - sh->depth[cur][a] >= p.window && cl.base + sh->depth[cur][a] >= p.sinks)
+        bits[a >> 5] &= ~(1u << (a & 31));
+  }
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  return cur;
+}
+
+// Joins the shares of a query tile's rows and writes them:
+// o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the CTAs c of the
+// cluster (one CTA: no cluster), four columns per thread; rows that saw
+// nothing get 0.  Every thread of the CTA calls it; a CTA leaves only when the
+// others have read its shared memory.
+template <int D>
+__device__ __forceinline__ void join_shares(const CacheAttnParams& p, CacheShared* sh, const uint8_t* smem, int bg,
+                                            int row0, int n_rows, int kr) {
+  constexpr int OPitch = CacheCfg<D>::OPitch;
+  const float* sO = reinterpret_cast<const float*>(smem);
+  const int share = blockIdx.x % p.n_split;
+  if (p.n_split > 1) {
+    __syncwarp();
+    cluster_sync();
+  }
+  const bool ok = *static_cast<volatile int*>(&sh->abort) == 0;
+  // S lanes (a power of two) take one four-column piece of a row, each S-th
+  // share, and U pieces at once (remote reads take about 0.6 us: with one piece
+  // in flight per lane, 128 rows of d = 128 in 3 shares took 8 us)
+  constexpr int U = 4;
+  int S = 1;
+  while (S * 2 <= p.n_split) S *= 2;
+  const int n_units = n_rows * (D / 4), per_cta = kCacheThreads / S;
+  const int sub = threadIdx.x % S;
+  for (int u0 = share * per_cta + threadIdx.x / S; __any_sync(0xffffffffu, u0 < n_units);
+       u0 += U * p.n_split * per_cta) {
+    float m[U][2], l[U][2];
+    float4 x[U][2];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = u0 + i * p.n_split * per_cta, er = u / (D / 4), c4 = u % (D / 4);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {      // n_split < 2 S: at most two shares per lane
+        const int c = sub + h * S;
+        m[i][h] = -INFINITY;
+        l[i][h] = 0.f;
+        x[i][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ok && u < n_units && c < p.n_split) {
+          if (p.n_split == 1) {
+            m[i][h] = sh->row_m[er];
+            l[i][h] = sh->row_l[er];
+            x[i][h] = reinterpret_cast<const float4*>(sO + er * OPitch)[c4];
+          } else {
+            m[i][h] = ld_cluster_f32(cluster_map(smem_u32(&sh->row_m[er]), c));
+            l[i][h] = ld_cluster_f32(cluster_map(smem_u32(&sh->row_l[er]), c));
+            x[i][h] = ld_cluster_f32x4(cluster_map(smem_u32(sO + er * OPitch + c4 * 4), c));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = u0 + i * p.n_split * per_cta, er = u / (D / 4), c4 = u % (D / 4);
+      float M = fmaxf(m[i][0], m[i][1]), Ls = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int o = 1; o < S; o *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (m[i][h] > -INFINITY) {       // else the share saw nothing and its O was not written
+          const float f = ex2(m[i][h] - M);
+          Ls = fmaf(l[i][h], f, Ls);
+          a.x = fmaf(x[i][h].x, f, a.x), a.y = fmaf(x[i][h].y, f, a.y);
+          a.z = fmaf(x[i][h].z, f, a.z), a.w = fmaf(x[i][h].w, f, a.w);
+        }
+      }
+      for (int o = 1; o < S; o *= 2) {
+        Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+        a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+        a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+      }
+      const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+      if (ok && u < n_units && sub == 0)
+        reinterpret_cast<uint2*>(row_ptr(p.o_routed, p.o_sh, p, bg, row0 + er, kr, D))[c4] =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    }
+  }
+  if (p.n_split > 1) {
+    __syncwarp();
+    cluster_sync_relaxed();
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kCacheThreads, 2)
 attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                   const __grid_constant__ CUtensorMap mapKt, const __grid_constant__ CUtensorMap mapVt,
                   CacheAttnParams p) {
   using C = CacheCfg<D>;
-  constexpr int KT = C::KT, ST = kCacheST;
+  constexpr int KT = C::KT, KST = C::KST, VST = C::VST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + C::QBytes;
-  uint8_t* sV = sK + ST * C::KVBytes;
-  CacheShared* sh = reinterpret_cast<CacheShared*>(sV + ST * C::KVBytes);
+  uint8_t* sV = sK + KST * C::KVBytes;
+  CacheShared* sh = reinterpret_cast<CacheShared*>(sV + VST * C::KVBytes);
   volatile int* abort = &sh->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -297,41 +432,38 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
   const int first = (int)((long long)cl.n * share / p.n_split);
   const int n = row0 / kr < cl.m ? (int)((long long)cl.n * (share + 1) / p.n_split) - first : 0;
 
-  const size_t item = blockIdx.x;
-  float* part_o = p.part + item * p.rows_cap * D;
-  float* part_ml = p.part + (size_t)gridDim.x * p.rows_cap * D + item * p.rows_cap * 2;
   if (n == 0) {
-    if (p.n_split == 1) {
-      for (int e = tid; e < n_rows * (D / 8); e += kCacheThreads)
-        reinterpret_cast<uint4*>(row_ptr(p.o_routed, p.o_sh, p, bg, row0 + e / (D / 8), kr, D))[e % (D / 8)] =
-            make_uint4(0, 0, 0, 0);
-    } else {
-      for (int e = tid; e < n_rows; e += kCacheThreads) {
-        part_ml[2 * e] = -INFINITY;
-        part_ml[2 * e + 1] = 0.f;
-      }
+    // an empty share: its rows saw nothing
+    for (int e = tid; e < n_rows; e += kCacheThreads) {
+      sh->row_m[e] = -INFINITY;
+      sh->row_l[e] = 0.f;
     }
+    if (tid == 0) sh->abort = 0;
+    __syncthreads();
+    join_shares<D>(p, sh, smem, bg, row0, n_rows, kr);
     return;
   }
 
   auto load_k = [&](int j) {
-    const int s = j % ST, i = first + j;
+    const int s = j % KST, i = first + j;
     const CUtensorMap* map = i < cl.n_cache ? &mapK : &mapKt;
     mbar_arrive_expect_tx(&sh->k_full[s], C::KVBytes);
     for (int bx = 0; bx < C::NB; ++bx)
       tma_load_3d(sK + s * C::KVBytes + bx * C::KBox, map, &sh->k_full[s], bx * 64, cl.row<KT>(i), bg);
   };
   auto load_v = [&](int j) {
-    const int s = j % ST, i = first + j;
+    const int s = j % VST, i = first + j;
     const CUtensorMap* map = i < cl.n_cache ? &mapV : &mapVt;
     mbar_arrive_expect_tx(&sh->v_full[s], C::KVBytes);
     for (int bx = 0; bx < C::NB; ++bx)
       tma_load_3d(sV + s * C::KVBytes + bx * C::KBox, map, &sh->v_full[s], bx * 64, cl.row<KT>(i), bg);
   };
   if (warp == 4 && lane == 0) {
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < KST; ++s) {
       mbar_init(&sh->k_full[s], 1);
       mbar_init(&sh->k_empty[s], 1);
+    }
+    for (int s = 0; s < VST; ++s) {
       mbar_init(&sh->v_full[s], 1);
       mbar_init(&sh->v_empty[s], 1);
     }
@@ -341,54 +473,30 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     mbar_init(&sh->pv_done, 1);
     sh->abort = 0;
     fence_mbar_init();
-    for (int j = 0; j < ST && j < n; ++j) {
+    for (int j = 0; j < KST && j < n; ++j) {
       load_k(j);
-      load_v(j);
+      if (j < VST) load_v(j);
     }
   }
   if (warp == 5) tmem_alloc(&sh->tmem_base, 256);
-  // Q rows, repeated `rep` times, into the 128-byte swizzled layout
-  for (int e = tid; e < kRowsQ * (D / 8); e += kCacheThreads) {
-    const int L = e / (D / 8), c = e % (D / 8), r = L % lanes_rep;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < n_rows) v = reinterpret_cast<const uint4*>(row_ptr(p.q_routed, p.q_sh, p, bg, row0 + r, kr, D))[c];
-    st_shared_v4(sQ + (c >> 3) * C::QBox + L * 128 + (((c & 7) ^ (L & 7)) << 4), v.x, v.y, v.z, v.w);
-  }
-  // ancestors and depths of the drafted tokens by pointer doubling: after round
-  // r a token's bits cover 2^(r+1) - 1 levels above it
-  int cur = 0;
-  if (p.tree) {
-    if (tid < p.T) {
-      int up = tid < cl.m ? p.parent[(size_t)b * p.T + tid] : -1;
-      if (up < -1 || up >= tid) {
-        if (p.err) atomicCAS(p.err, 0u, (unsigned)kErrTreeArgs);
-        up = -1;
-      }
+  const int up = p.tree && tid < cl.m ? p.parent[(size_t)b * p.T + tid] : -1;
+  // Q rows, repeated `rep` times, into the 128-byte swizzled layout (every load
+  // in flight before the first store: one trip to memory)
+  {
+    constexpr int NL = (kRowsQ * (D / 8) + kCacheThreads - 1) / kCacheThreads;
+    uint4 v[NL];
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        sh->anc[0][tid][w] = ((tid >> 5) == w ? 1u << (tid & 31) : 0u) |
-                             (up >= 0 && (up >> 5) == w ? 1u << (up & 31) : 0u);
-      sh->up[0][tid] = up;
-      sh->depth[0][tid] = up >= 0 ? 1 : 0;
+    for (int i = 0; i < NL; ++i) {
+      const int e = tid + i * kCacheThreads, r = e / (D / 8);
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r < n_rows) v[i] = reinterpret_cast<const uint4*>(row_ptr(p.q_routed, p.q_sh, p, bg, row0 + r, kr, D))[e % (D / 8)];
     }
-    for (int span = 1; span < p.T; span *= 2) {
-      __syncthreads();
-      if (tid < p.T) {
-        const int up = sh->up[cur][tid];
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
-          sh->anc[cur ^ 1][tid][w] = sh->anc[cur][tid][w] | (up >= 0 ? sh->anc[cur][up][w] : 0u);
-        sh->depth[cur ^ 1][tid] = sh->depth[cur][tid] + (up >= 0 ? sh->depth[cur][up] : 0);
-        sh->up[cur ^ 1][tid] = up >= 0 ? sh->up[cur][up] : -1;
-      }
-      cur ^= 1;
-    }
-    __syncthreads();
-    if (p.window && p.window < p.T && tid < p.T) {
-      // ancestors that the window has left behind
-      for (int a = 0; a < tid; ++a)
-        if (sh->depth[cur][tid] - sh->depth[cur][a] >= p.window && cl.base + sh->depth[cur][a] >= p.sinks)
-          sh->anc[cur][tid][a >> 5] &= ~(1u << (a & 31));
+    for (int i = 0; i < NL; ++i) {
+      const int e = tid + i * kCacheThreads, c = e % (D / 8);
+      if (e / (D / 8) < lanes_rep)
+        for (int L = e / (D / 8); L < kRowsQ; L += lanes_rep)
+          st_shared_v4(sQ + (c >> 3) * C::QBox + L * 128 + (((c & 7) ^ (L & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
     }
   }
   fence_proxy_async_smem();
@@ -403,9 +511,9 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
       const uint32_t q0 = smem_u32(sQ);
       bool ok = true;
       for (int j = 0; ok && j < n; ++j) {
-        const int s = j % ST;
+        const int s = j % KST;
         if (j > 0) ok = mbar_wait(&sh->s_free, (j - 1) & 1, abort, p.err, kErrTimeoutCacheAttn);
-        ok = ok && mbar_wait(&sh->k_full[s], (j / ST) & 1, abort, p.err, kErrTimeoutCacheAttn);
+        ok = ok && mbar_wait(&sh->k_full[s], (j / KST) & 1, abort, p.err, kErrTimeoutCacheAttn);
         if (!ok) break;
         tc_fence_after();
         const uint32_t k0 = smem_u32(sK + s * C::KVBytes);
@@ -415,10 +523,10 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
                   sdesc_sw128(k0 + (ks >> 2) * C::KBox + (ks & 3) * 32, 16, 1024), idesc_s, ks > 0);
         umma_commit(&sh->s_full);
         umma_commit(&sh->k_empty[s]);
-        if (j + ST < n) {
-          ok = mbar_wait(&sh->k_empty[s], (j / ST) & 1, abort, p.err, kErrTimeoutCacheAttn);
+        if (j + KST < n) {
+          ok = mbar_wait(&sh->k_empty[s], (j / KST) & 1, abort, p.err, kErrTimeoutCacheAttn);
           if (!ok) break;
-          load_k(j + ST);
+          load_k(j + KST);
         }
       }
     }
@@ -426,9 +534,9 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     if (lane == 0) {
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRowsQ, D, false, true);
       for (int j = 0; j < n; ++j) {
-        const int s = j % ST;
+        const int s = j % VST;
         if (!mbar_wait(&sh->p_full, j & 1, abort, p.err, kErrTimeoutCacheAttn)) break;
-        if (!mbar_wait(&sh->v_full[s], (j / ST) & 1, abort, p.err, kErrTimeoutCacheAttn)) break;
+        if (!mbar_wait(&sh->v_full[s], (j / VST) & 1, abort, p.err, kErrTimeoutCacheAttn)) break;
         tc_fence_after();
         const uint32_t v0 = smem_u32(sV + s * C::KVBytes);
 #pragma unroll
@@ -437,20 +545,21 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
                   (j > 0 || ks > 0));
         umma_commit(&sh->pv_done);
         umma_commit(&sh->v_empty[s]);
-        if (j + ST < n) {
-          if (!mbar_wait(&sh->v_empty[s], (j / ST) & 1, abort, p.err, kErrTimeoutCacheAttn)) break;
-          load_v(j + ST);
+        if (j + VST < n) {
+          if (!mbar_wait(&sh->v_empty[s], (j / VST) & 1, abort, p.err, kErrTimeoutCacheAttn)) break;
+          load_v(j + VST);
         }
       }
     }
   } else {
     // ---------------- softmax: warps 0-3, one lane per (row, repeat)
+    const int cur = p.tree ? build_tree(p, cl, sh, up) : 0;
     const int r = tid % lanes_rep, q = tid / lanes_rep;
     const int t_r = (row0 + r) / kr;
     const bool live = r < n_rows && t_r < cl.m;
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const int depth = p.tree && live ? sh->depth[cur][t_r] : 0;
-    const uint32_t* anc = sh->anc[cur][live ? t_r : 0];
+    const uint32_t* anc = reinterpret_cast<const uint32_t*>(&sh->anc[cur][live ? t_r : 0]);
     RowState st;
     if (rep == 4)
       st = cache_softmax<D, KT / 4>(p, cl, sh, sV, lane_base, first, n, q * (KT / 4), t_r, anc, depth);
@@ -481,33 +590,22 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
       }
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
-    const bool aborted = *abort != 0;
-    for (int e = tid; e < n_rows * (D / 8) && !aborted; e += 128) {
-      const int er = e / (D / 8), c8 = e % (D / 8);
-      float a[8] = {}, Ls = 0.f, Ms = -INFINITY;
-      for (int i = 0; i < rep; ++i) {
-        const int L = er + i * lanes_rep;
-        const float4 x = reinterpret_cast<const float4*>(sO + L * C::OPitch)[c8 * 2];
-        const float4 y = reinterpret_cast<const float4*>(sO + L * C::OPitch)[c8 * 2 + 1];
-        a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
-        a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
-        Ls += sh->l[L];
-        Ms = fmaxf(Ms, sh->m[L]);
+    // the sum over a row's repeats replaces its first repeat
+    for (int e = tid; rep > 1 && e < n_rows * (D / 4); e += 128) {
+      const int er = e / (D / 4), c4 = e % (D / 4);
+      float4* first_o = reinterpret_cast<float4*>(sO + er * C::OPitch) + c4;
+      float4 a = *first_o;
+      for (int i = 1; i < rep; ++i) {
+        const float4 x = reinterpret_cast<const float4*>(sO + (er + i * lanes_rep) * C::OPitch)[c4];
+        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
       }
-      if (p.n_split == 1) {
-        const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-        reinterpret_cast<uint4*>(row_ptr(p.o_routed, p.o_sh, p, bg, row0 + er, kr, D))[c8] =
-            make_uint4(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv),
-                       pack_bf16x2(a[4] * inv, a[5] * inv), pack_bf16x2(a[6] * inv, a[7] * inv));
-      } else {
-        float4* d4 = reinterpret_cast<float4*>(part_o + er * D + c8 * 8);
-        d4[0] = make_float4(a[0], a[1], a[2], a[3]);
-        d4[1] = make_float4(a[4], a[5], a[6], a[7]);
-        if (c8 == 0) {
-          part_ml[2 * er] = Ms;
-          part_ml[2 * er + 1] = Ls;
-        }
-      }
+      *first_o = a;
+    }
+    if (tid < n_rows) {
+      float Ls = 0.f;
+      for (int i = 0; i < rep; ++i) Ls += sh->l[tid + i * lanes_rep];
+      sh->row_m[tid] = M;
+      sh->row_l[tid] = Ls;
     }
   }
   tc_fence_before();
@@ -516,42 +614,8 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
+  join_shares<D>(p, sh, smem, bg, row0, n_rows, kr);
   drain_after_abort(abort);
-}
-
-// Joins the shares of every row: o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
-// Eight columns per thread; rows that saw nothing get 0.
-template <int D>
-__global__ void __launch_bounds__(256) attn_cache_merge_kernel(CacheAttnParams p, long long n_items) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int c8 = (int)(e % (D / 8));
-  const int r = (int)(e / (D / 8) % p.rows_cap);
-  const long long tile = e / (D / 8) / p.rows_cap;      // (b, g, query tile)
-  if (tile * p.n_split >= n_items) return;
-  const int bg = (int)(tile / p.n_qt), row0 = (int)(tile % p.n_qt) * kRowsQ;
-  const int kr = p.k + (p.n_shared && bg % p.G == p.sg ? 1 : 0);
-  if (row0 + r >= p.T * kr) return;
-  const float* ml = p.part + (size_t)n_items * p.rows_cap * D + ((size_t)tile * p.n_split * p.rows_cap + r) * 2;
-  const float* po = p.part + ((size_t)tile * p.n_split * p.rows_cap + r) * D + c8 * 8;
-  float M = -INFINITY;
-  for (int c = 0; c < p.n_split; ++c) M = fmaxf(M, ml[(size_t)c * p.rows_cap * 2]);
-  float a[8] = {}, Ls = 0.f;
-  for (int c = 0; c < p.n_split; ++c) {
-    const float mc = ml[(size_t)c * p.rows_cap * 2];
-    if (mc == -INFINITY) continue;         // nothing seen: its O was not written
-    const float f = ex2(mc - M);
-    const float4 x = reinterpret_cast<const float4*>(po + (size_t)c * p.rows_cap * D)[0];
-    const float4 y = reinterpret_cast<const float4*>(po + (size_t)c * p.rows_cap * D)[1];
-    Ls = fmaf(ml[(size_t)c * p.rows_cap * 2 + 1], f, Ls);
-    a[0] = fmaf(x.x, f, a[0]), a[1] = fmaf(x.y, f, a[1]), a[2] = fmaf(x.z, f, a[2]), a[3] = fmaf(x.w, f, a[3]);
-    a[4] = fmaf(y.x, f, a[4]), a[5] = fmaf(y.y, f, a[5]), a[6] = fmaf(y.z, f, a[6]), a[7] = fmaf(y.w, f, a[7]);
-  }
-  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-  reinterpret_cast<uint4*>(row_ptr(p.o_routed, p.o_sh, p, bg, row0 + r, kr, D))[c8] =
-      make_uint4(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv),
-                 pack_bf16x2(a[4] * inv, a[5] * inv), pack_bf16x2(a[6] * inv, a[7] * inv));
 }
 
 // Accepted drafted rows to the end of the cache: one CTA per sequence, so that
@@ -602,26 +666,23 @@ void cache_attn_plan(int B, int T, int G, int k, int n_shared, int d, int L_max,
   const int KT = d == 64 ? 128 : 64;
   const int rows = T * (k + n_shared);
   P->n_qt = (rows + kRowsQ - 1) / kRowsQ;
-  P->rows_cap = rows < kRowsQ ? rows : kRowsQ;
-  // Shares per query tile: the fewest that come within a twentieth of the
-  // shortest time of ceil(items * shares / slots) waves of (tiles per share +
-  // start-up) each; 296 slots are two CTAs on each of 148 SMs, and a CTA's
-  // start-up and end cost about as much as four tiles.
+  // Shares per query tile (the CTAs of a cluster: at most 16), by a model of the
+  // time in units of one key tile of a CTA that has its SM to itself (about
+  // 1 us): start-up and end 5, a tile 4/3 when two CTAs share an SM, a quarter
+  // for each CTA of the cluster's barriers, all of it once per 296 CTAs (two on
+  // each of 148 SMs) but at least once.  Measured (us): 64 x 8 items of 33 tiles
+  // 95, 109, 121 for 1, 2, 3 shares; 20 items of 17 tiles 14.2, 11.2, 9.9, 11.2,
+  // 19 for 2, 4, 6, 8, 16; 72 items of 35 tiles 36, 33, 51 for 2, 3, 4; 8 items
+  // of 33 tiles 20, 14.6, 11.7, 11.7 for 2, 4, 6, 16.
   const long long items = (long long)B * G * P->n_qt, nt = max_tiles(L_max, T, tree, window, sinks, KT);
-  const long long slots = 296, startup = 4;
-  long long best = 0;
-  int cap = (int)(nt < 32 ? nt : 32);
-  auto cost = [&](int n) { return (items * n + slots - 1) / slots * ((nt + n - 1) / n + startup); };
-  for (int n = 1; n <= cap; ++n)
-    if (n == 1 || cost(n) < best) best = cost(n);
-  P->n_split = 1;
-  for (int n = 1; n <= cap; ++n)
-    if (cost(n) * 20 <= best * 21) {
-      P->n_split = n;
-      break;
-    }
+  const int cap = (int)(nt < 16 ? nt : 16);
+  double best = 0;
+  for (int n = 1; n <= cap; ++n) {
+    const double ctas = (double)items * n, tiles = (double)((nt + n - 1) / n);
+    const double cost = (5 + tiles * (ctas > 148 ? 4.0 / 3 : 1.0) + 0.25 * n) * (ctas > 296 ? ctas / 296 : 1.0);
+    if (n == 1 || cost < best) best = cost, P->n_split = n;
+  }
   P->items = items * P->n_split;
-  P->bytes = P->n_split == 1 ? 0 : (size_t)P->items * P->rows_cap * (d + 2) * sizeof(float);
 }
 
 template <int D>
@@ -629,13 +690,10 @@ static cudaError_t launch_cache(const CUtensorMap& mK, const CUtensorMap& mV, co
                                 const CUtensorMap& mVt, const CacheAttnParams& p, long long items,
                                 cudaStream_t stream) {
   auto kern = attn_cache_kernel<D>;
-  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), cache_smem<D>());
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), cache_smem<D>(), p.n_split > 8);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(kern, dim3((unsigned)items), dim3(kCacheThreads), cache_smem<D>(), stream, 1, mK, mV, mKt, mVt, p);
-  if (e != cudaSuccess || p.n_split == 1) return e;
-  const long long threads = items / p.n_split * p.rows_cap * (D / 8);
-  return launch_kernel(attn_cache_merge_kernel<D>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, 1, p,
-                       items);
+  return launch_kernel(kern, dim3((unsigned)items), dim3(kCacheThreads), cache_smem<D>(), stream, p.n_split, mK, mV, mKt,
+                       mVt, p);
 }
 
 cudaError_t launch_attn_cache(const CUtensorMap& mK, const CUtensorMap& mV, const CUtensorMap& mKt,

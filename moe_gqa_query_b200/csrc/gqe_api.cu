@@ -590,7 +590,8 @@ static gqe_status cache_attn_common(const gqe_dims* dims, const gqe_bf16* q_rout
   const int B = dims->B, T = dims->T, G = dims->G, k = dims->k, d = dims->d_head;
   CacheAttnPlan P;
   cache_attn_plan(B, T, G, k, dims->n_shared, d, L_max, tree, window, sinks, &P);
-  GQE_REQUIRE(P.bytes == 0 || (ws && aligned16(ws) && ws_bytes >= P.bytes), GQE_ERR_WORKSPACE);
+  (void)ws;            // the shares are joined on chip: no scratch (gqe_window_workspace_size says 0)
+  (void)ws_bytes;
   GQE_REQUIRE(P.items <= 0x7FFFFFFFll, GQE_ERR_UNSUPPORTED);
   const uint32_t box = cache_attn_key_tile(d);
   CUtensorMap mK, mV, mKt, mVt;
@@ -611,7 +612,6 @@ static gqe_status cache_attn_common(const gqe_dims* dims, const gqe_bf16* q_rout
   p.cache_len = cache_len;
   p.parent = parent;
   p.tree_len = tree_len;
-  p.part = static_cast<float*>(ws);
   p.B = B;
   p.T = T;
   p.G = G;
@@ -624,7 +624,6 @@ static gqe_status cache_attn_common(const gqe_dims* dims, const gqe_bf16* q_rout
   p.sinks = sinks;
   p.n_qt = P.n_qt;
   p.n_split = P.n_split;
-  p.rows_cap = P.rows_cap;
   p.scale_log2 = scale_log2(dims);
   p.err = error_word();
   return cuda_status(launch_attn_cache(mK, mV, mKt, mVt, p, d, P.items, S(stream)));
@@ -688,9 +687,7 @@ gqe_status gqe_window_workspace_size(const gqe_dims* dims, int op, int L_max, in
     GQE_REQUIRE(L_max >= 1, GQE_ERR_INVALID_ARG);
     if (tree) GQE_REQUIRE(T <= kMaxTree, GQE_ERR_UNSUPPORTED);
     else GQE_REQUIRE(T == 1, GQE_ERR_INVALID_ARG);
-    CacheAttnPlan P;
-    cache_attn_plan(B, T, G, k, dims->n_shared, d, L_max, tree, window, sinks, &P);
-    *bytes = P.bytes;
+    *bytes = 0;
     return GQE_OK;
   }
   return GQE_ERR_INVALID_ARG;

@@ -1,5 +1,6 @@
-// launch.cuh -- host helpers: raise a kernel's dynamic shared-memory limit once
-// per (kernel, device, size) instead of on every launch; launch a kernel with
+// launch.cuh -- host helpers: raise a kernel's dynamic shared-memory limit (and
+// allow clusters past the portable 8 CTAs) once per (kernel, device, size)
+// instead of on every launch; launch a kernel with
 // programmatic dependent launch (and optionally as clusters).
 #pragma once
 
@@ -11,11 +12,12 @@
 
 namespace gqe {
 
-inline cudaError_t ensure_smem(const void* kern, size_t bytes) {
+inline cudaError_t ensure_smem(const void* kern, size_t bytes, bool wide_cluster = false) {
   struct Entry {
     const void* kern;
     int dev;
     size_t bytes;
+    bool wide;
   };
   static std::mutex mu;
   static std::vector<Entry> done;
@@ -25,12 +27,16 @@ inline cudaError_t ensure_smem(const void* kern, size_t bytes) {
   {
     std::lock_guard<std::mutex> lock(mu);
     for (const Entry& x : done)
-      if (x.kern == kern && x.dev == dev && x.bytes >= bytes) return cudaSuccess;
+      if (x.kern == kern && x.dev == dev && x.bytes >= bytes && x.wide >= wide_cluster) return cudaSuccess;
   }
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
+  if (wide_cluster) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   std::lock_guard<std::mutex> lock(mu);
-  done.push_back({kern, dev, bytes});
+  done.push_back({kern, dev, bytes, wide_cluster});
   return cudaSuccess;
 }
 
