@@ -7,6 +7,12 @@ namespace gqe {
 
 typedef uint16_t gqe_bf16_t;
 
+// Bits i of a 32-position word at position pos with pos + i < x.
+__device__ __forceinline__ uint32_t bits_below(int x, int pos) {
+  const int n = min(max(x - pos, 0), 32);
+  return n == 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
 struct AttnParams {
   gqe_bf16_t* o_routed;   // [B, G, T, k, d]
   gqe_bf16_t* o_sh;       // [B, T, d]
@@ -23,7 +29,9 @@ cudaError_t launch_debug_wait(unsigned* err, cudaStream_t stream);
 cudaError_t launch_attn_prefill(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
                                 const CUtensorMap& mV, const AttnParams& p, int d,
                                 cudaStream_t stream);
-// The same attention under a sliding window with sinks (p.window, p.sinks).
+// The same attention under a sliding window with sinks (p.window, p.sinks);
+// the K and V maps' boxes hold attn_window_key_tile(d) rows.
+constexpr int attn_window_key_tile(int d) { return d == 64 ? 128 : 64; }
 cudaError_t launch_attn_prefill_window(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
                                        const CUtensorMap& mV, const AttnParams& p, int d, cudaStream_t stream);
 
@@ -54,8 +62,8 @@ struct AttnBwdParams {
   const gqe_bf16_t* o_sh;           // [B, T, d]
   const gqe_bf16_t* do_routed;
   const gqe_bf16_t* do_sh;
-  float* lse2;                      // [n_rows_pad] LSE * log2(e), +inf on padding
-  float* delta;                     // [n_rows_pad] sum_c dO * O
+  float* lse2;                      // [n_rows_pad] LSE * log2(e), +inf on padding (windowed: negated)
+  float* delta;                     // [n_rows_pad] sum_c dO * O (windowed: negated)
   float* dq_acc;                    // [n_rows_pad, d] fp32
   gqe_bf16_t* dq_routed;            // [B, G, T, k, d]
   gqe_bf16_t* dq_sh;                // [B, T, d]
@@ -66,13 +74,9 @@ struct AttnBwdParams {
   long long n_rows_pad;
   float scale, scale_log2;
   unsigned* err;
-  // windowed launches only: 1 <= window <= T, 0 <= sinks <= T, and the split of
-  // the sink tiles' walks
+  // windowed launches only: 1 <= window <= T, 0 <= sinks <= T
   int window, sinks;
-  int sink_tiles;                   // key tiles that hold sinks and are split (0: none)
-  int split_len;                    // query tiles per part of a split walk
-  int n_parts;                      // parts per sink tile (the last ones may be empty)
-  float* part;                      // [sink_tiles, B*G, n_parts, 2 (dK, dV), 128, d] fp32
+  float* part;                      // cut walks' sums: [2 * CTAs, 2 (dK, dV), 128, d] fp32
 };
 
 struct AttnBwdLayout {
@@ -81,18 +85,25 @@ struct AttnBwdLayout {
   size_t off_lse2, off_delta, off_dq, bytes;
 };
 
-// Windowed backward: how the sink tiles' long walks are split, and the scratch
-// (attn_bwd_layout's, then the parts).
-struct AttnBwdWindowPlan {
-  int sink_tiles, split_len, n_parts;
-  size_t off_part, bytes;
-};
+cudaError_t launch_attn_bwd_prep(const AttnBwdParams& p, cudaStream_t stream);
+cudaError_t launch_attn_bwd_post(const AttnBwdParams& p, cudaStream_t stream);
 
-void attn_bwd_window_plan(int B, int T, int G, int k, int n_shared, int d, int window, int sinks,
-                          AttnBwdWindowPlan* P);
+// Windowed backward (attn_bwd_window.cu): where each CTA starts in the list of
+// (sequence, key tile, query tile of its walk), cut into equal stretches.
+constexpr int kBwdWindowCtas = 148;
+struct AttnBwdSchedule {
+  int n_ctas;
+  int seq[kBwdWindowCtas + 1], jt[kBwdWindowCtas + 1], off[kBwdWindowCtas + 1];
+  int count[kBwdWindowCtas];        // query tiles of each CTA
+};
+// The schedule, the bytes of scratch (attn_bwd_layout's, then the cut walks'
+// sums) and where the sums lie.
+void attn_bwd_window_plan(int B, int T, int G, int k, int n_shared, int sg, int d, int window, int sinks,
+                          AttnBwdSchedule* S, size_t* off_part, size_t* bytes);
 cudaError_t launch_attn_bwd_window(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
                                    const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
-                                   const CUtensorMap& mdQ, const AttnBwdParams& p, cudaStream_t stream);
+                                   const CUtensorMap& mdQ, const AttnBwdParams& p, const AttnBwdSchedule& S,
+                                   cudaStream_t stream);
 
 void attn_bwd_layout(int B, int T, int G, int k, int n_shared, int d, AttnBwdLayout* L);
 cudaError_t launch_attn_bwd(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
@@ -126,8 +137,7 @@ struct CacheAttnPlan {
 
 void cache_attn_plan(int B, int T, int G, int k, int n_shared, int d, int L_max, bool tree, int window, int sinks,
                      CacheAttnPlan* P);
-// Key rows per TMA box of the K and V maps.
-constexpr int cache_attn_key_tile(int d) { return d == 64 ? 128 : 64; }
+// (the K and V maps' boxes hold attn_window_key_tile(d) rows)
 cudaError_t launch_attn_cache(const CUtensorMap& mK, const CUtensorMap& mV, const CUtensorMap& mKt,
                               const CUtensorMap& mVt, const CacheAttnParams& p, int d, long long items,
                               cudaStream_t stream);

@@ -40,15 +40,6 @@
 // dQ_i accumulates over dP^T's columns once the warpgroups have read them, so
 // dP^T(i+1) waits for dQ_i to be drained and S^T(i+1) for dK_i.  dO has a
 // one-stage ring here (shared memory holds K, V, two Q stages, dO and dS).
-//
-// Sliding window with sinks (WIN instances; query t sees key p when p <= t and
-// (p > t - window or p < sinks)): key tile j walks the query tiles from token
-// 128 j up to the last token whose window reaches its last key, and to the end
-// when it holds a sink.  The sink tiles' walks are then the longest by far
-// (T / 128 query tiles against window / 128 + 1), so they are cut into parts
-// of split_len query tiles, one CTA each: every part writes its dK, dV sums in
-// fp32 into a slot of its own and attn_bwd_sink_sum_kernel adds the slots in
-// their order, so dK and dV do not depend on timing.
 #include "attn.cuh"
 #include "launch.cuh"
 
@@ -142,14 +133,7 @@ __device__ __forceinline__ uint32_t dst_wcol(int w) {
   return D == 64 ? BwdCfg<D>::kDP + 64 * w : BwdCfg<D>::kS + 64 + 32 * w;
 }
 
-// Query tiles (routed, then shared) that key tile jt of group g sees.
-__device__ __forceinline__ void walk_counts(const AttnBwdParams& p, bool win, int jt, int g, int* n_r, int* n_s) {
-  const int t_hi = win && jt * kTileB >= p.sinks ? min(p.T - 1, jt * kTileB + kTileB - 2 + p.window) : p.T - 1;
-  *n_r = ((t_hi + 1) * p.k + kTileB - 1) / kTileB - jt * p.k;
-  *n_s = (p.n_shared && g == p.sg) ? t_hi / kTileB + 1 - jt : 0;
-}
-
-template <int D, bool WIN>
+template <int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapQs,
                 const __grid_constant__ CUtensorMap mapdO, const __grid_constant__ CUtensorMap mapdOs,
@@ -170,23 +154,13 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
   // ---- work item: key tile jt of sequence s, key tiles in ascending order
   // (tile 0 sees the most query tiles: heaviest first)
   const int BG = p.B * p.G;
-  int item = (int)blockIdx.x / BG, part = 0;
-  if (WIN && p.sink_tiles > 0) {
-    // sink tiles first, n_parts CTAs each, then one CTA per other key tile
-    const int n_split = p.sink_tiles * p.n_parts;
-    part = item < n_split ? item % p.n_parts : 0;
-    item = item < n_split ? item / p.n_parts : item - n_split + p.sink_tiles;
-  }
-  const int jt = item;
+  const int jt = (int)blockIdx.x / BG;
   const int s = (int)blockIdx.x % BG;
   const int g = s % p.G;
-  int n_r, n_s;
-  walk_counts(p, WIN, jt, g, &n_r, &n_s);
-  // this CTA's stretch of the walk: query tiles [q_first, q_first + cnt)
-  const bool split = WIN && jt < p.sink_tiles;
-  const int q_first = split ? part * p.split_len : 0;
-  const int cnt = split ? min(p.split_len, n_r + n_s - q_first) : n_r + n_s;
-  if (WIN && cnt <= 0) return;
+  const int nq_r = (p.T * p.k + kTileB - 1) / kTileB;
+  const int n_r = nq_r - jt * p.k;
+  const int n_s = (p.n_shared && g == p.sg) ? (p.T + kTileB - 1) / kTileB - jt : 0;
+  const int cnt = n_r + n_s;
   const float sl2 = p.scale_log2;
 
   if (threadIdx.x == 0) {
@@ -233,7 +207,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
       for (int n = 0; n < cnt; ++n) {
         const int st = n & 1;
         if (n >= 2 && !mbar_wait(&bar->q_empty[st], ((n >> 1) - 1) & 1, abort, p.err, kErrTimeoutAttnBwd)) break;
-        const QTile q = qtile(p, s, jt, n_r, q_first + n);
+        const QTile q = qtile(p, s, jt, n_r, n);
         const CUtensorMap* mq = q.shared ? &mapQs : &mapQ;
         const CUtensorMap* mo = q.shared ? &mapdOs : &mapdO;
         const int seq = q.shared ? s / p.G : s;
@@ -368,7 +342,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     bool ok = true;
     for (int n = 0; n < cnt && ok; ++n) {
       const int st = n & 1;
-      const QTile q = qtile(p, s, jt, n_r, q_first + n);
+      const QTile q = qtile(p, s, jt, n_r, n);
       ok = mbar_wait(&bar->q_full[st], (n >> 1) & 1, abort, p.err, kErrTimeoutAttnBwd);
       ok = ok && mbar_wait(&bar->s_full, n & 1, abort, p.err, kErrTimeoutAttnBwd);
       if (!C::kWide && !ok) break;
@@ -401,15 +375,6 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (c < cmin) pf[c] = 0.f;
-      }
-      if (WIN) {
-        // query columns c >= cmax belong to tokens whose window starts behind this key
-        const int cmax = kv_pos < p.sinks ? kTileB : (kv_pos + p.window) * q.kk - q.i * kTileB - (int)col0;
-        if (cmax < 64) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c >= cmax) pf[c] = 0.f;
-        }
       }
       if (!C::kWide) {
         // P^T(n-1) must have been read by dV(n-1) before P^T(n) replaces it
@@ -504,7 +469,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     for (int n = 0; n < cnt && ok; ++n) {
       const int b = 0;
       const int ph = n & 1;
-      const QTile q = qtile(p, s, jt, n_r, q_first + n);
+      const QTile q = qtile(p, s, jt, n_r, n);
       ok = mbar_wait(&bar->dq_full[b], ph, abort, p.err, kErrTimeoutAttnBwd);
       if (!ok) break;
       tc_fence_after();
@@ -544,24 +509,6 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     tc_fence_after();
     const int kv_pos = jt * kTileB + qd * 32 + lane;
     const size_t orow = ((size_t)s * p.T + kv_pos) * D;
-    if (split) {
-      float* slot = p.part + (((size_t)jt * BG + s) * p.n_parts + part) * 2 * kTileB * D;
-#pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        float* dst = slot + ((size_t)which * kTileB + qd * 32 + lane) * D;
-        const uint32_t col = which ? C::kDV : C::kDK;
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(tmem + lane_off + col + c0, v);
-          if (ok) {
-            uint4* d4 = reinterpret_cast<uint4*>(dst + c0);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) d4[c] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-          }
-        }
-      }
-    } else
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       gqe_bf16_t* dst = (which ? p.dV : p.dK) + orow;
@@ -633,8 +580,9 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(AttnBwdParams p) {
   acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
   acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (part == 0) {
-    p.delta[pr] = valid ? dot : 0.f;
-    p.lse2[pr] = valid ? p.lse[src] * 1.4426950408889634f : INFINITY;
+    const float sgn = p.window ? -1.f : 1.f;       // the windowed kernel adds both
+    p.delta[pr] = valid ? dot * sgn : 0.f;
+    p.lse2[pr] = (valid ? p.lse[src] * 1.4426950408889634f : INFINITY) * sgn;
   }
 }
 
@@ -661,39 +609,13 @@ __global__ void __launch_bounds__(256) attn_bwd_post_kernel(AttnBwdParams p) {
     dst = p.dq_sh + ((long long)b * p.T + r) * p.d;
   }
   const float4* a = reinterpret_cast<const float4*>(p.dq_acc + pr * p.d + part * 8);
-  const float4 x = a[0], y = a[1];
+  float4 x = a[0], y = a[1];
+  if (p.window) {      // the windowed kernel leaves the scale of dS to this place
+    x.x *= p.scale, x.y *= p.scale, x.z *= p.scale, x.w *= p.scale;
+    y.x *= p.scale, y.y *= p.scale, y.z *= p.scale, y.w *= p.scale;
+  }
   reinterpret_cast<uint4*>(dst)[part] =
       make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-}
-
-// dK, dV of the sink tiles: the parts of each walk added in their order and
-// rounded.  Eight columns per thread.
-__global__ void __launch_bounds__(256) attn_bwd_sink_sum_kernel(AttnBwdParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int tpr = p.d / 8, BG = p.B * p.G;
-  const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const int c8 = (int)(gt % tpr);
-  const int row = (int)(gt / tpr % kTileB);
-  const int which = (int)(gt / tpr / kTileB % 2);
-  const long long seq = gt / tpr / kTileB / 2;      // sink tile * BG + sequence
-  if (seq >= (long long)p.sink_tiles * BG) return;
-  const int jt = (int)(seq / BG), s = (int)(seq % BG);
-  const int kv_pos = jt * kTileB + row;
-  if (kv_pos >= p.T) return;
-  int n_r, n_s;
-  walk_counts(p, true, jt, s % p.G, &n_r, &n_s);
-  const int parts = (n_r + n_s + p.split_len - 1) / p.split_len;
-  const float* src = p.part + ((seq * p.n_parts * 2 + which) * kTileB + row) * p.d + c8 * 8;
-  float a[8] = {};
-  for (int q = 0; q < parts; ++q, src += 2 * kTileB * p.d) {
-    const float4 x = reinterpret_cast<const float4*>(src)[0], y = reinterpret_cast<const float4*>(src)[1];
-    a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
-    a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
-  }
-  gqe_bf16_t* dst = (which ? p.dV : p.dK) + ((size_t)s * p.T + kv_pos) * p.d;
-  reinterpret_cast<uint4*>(dst)[c8] =
-      make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
 }
 
 }  // namespace
@@ -712,72 +634,31 @@ void attn_bwd_layout(int B, int T, int G, int k, int n_shared, int d, AttnBwdLay
   L->bytes = o;
 }
 
-// The sink tiles' walks are split only while they are few: past two CTAs per
-// SM of them they fill the GPU on their own, and the parts' scratch would grow
-// with the sinks.  A part is as long as an ordinary key tile's walk (at least
-// 16 query tiles, so that a part's dK, dV stores stay small next to its work),
-// and there are at most four parts per SM in all.
-void attn_bwd_window_plan(int B, int T, int G, int k, int n_shared, int d, int window, int sinks,
-                          AttnBwdWindowPlan* P) {
-  AttnBwdLayout L;
-  attn_bwd_layout(B, T, G, k, n_shared, d, &L);
-  constexpr int kSms = 148;
-  *P = AttnBwdWindowPlan{};
-  P->off_part = (L.bytes + 255) & ~size_t(255);
-  P->bytes = L.bytes;
-  const int tiles_t = (T + kTileB - 1) / kTileB;
-  const long long sink_tiles = (sinks + kTileB - 1) / kTileB, items = sink_tiles * B * G;
-  if (items == 0 || items >= 2 * kSms) return;
-  const int walk = (T * k + kTileB - 1) / kTileB + (n_shared ? tiles_t : 0);   // the longest sink tile's
-  const int len_w = ((window + kTileB - 2) / kTileB + 1) * k;
-  int parts = (int)((4 * kSms + items - 1) / items);
-  int len = (walk + parts - 1) / parts;
-  if (len < len_w) len = len_w;
-  if (len < 16) len = 16;
-  parts = (walk + len - 1) / len;
-  if (parts < 2) return;
-  P->sink_tiles = (int)sink_tiles;
-  P->split_len = len;
-  P->n_parts = parts;
-  P->bytes = P->off_part + (size_t)items * parts * 2 * kTileB * d * sizeof(float);
+cudaError_t launch_attn_bwd_prep(const AttnBwdParams& p, cudaStream_t stream) {
+  const long long threads = p.n_rows_pad * (p.d / 8);
+  return launch_kernel(attn_bwd_prep_kernel, dim3((int)((threads + 255) / 256)), dim3(256), 0, stream, 1, p);
 }
 
-template <bool WIN>
-static cudaError_t launch_bwd(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
-                              const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
-                              const CUtensorMap& mdQ, const AttnBwdParams& p, cudaStream_t stream) {
-  if (p.d != 64 && p.d != 128) return cudaErrorNotSupported;
+cudaError_t launch_attn_bwd_post(const AttnBwdParams& p, cudaStream_t stream) {
   const long long threads = p.n_rows_pad * (p.d / 8);
-  const int blocks = (int)((threads + 255) / 256);
-  cudaError_t e = launch_kernel(attn_bwd_prep_kernel, dim3(blocks), dim3(256), 0, stream, 1, p);
-  if (e != cudaSuccess) return e;
-  auto kern = p.d == 64 ? attn_bwd_kernel<64, WIN> : attn_bwd_kernel<128, WIN>;
-  const size_t smem = p.d == 64 ? BwdCfg<64>::Smem : BwdCfg<128>::Smem;
-  e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
-  if (e != cudaSuccess) return e;
-  int items = (p.T + kTileB - 1) / kTileB;
-  if (WIN && p.sink_tiles > 0) items += p.sink_tiles * (p.n_parts - 1);
-  e = launch_kernel(kern, dim3(items * p.B * p.G), dim3(kBwdThreads), smem, stream, 1, mQ, mQs, mdO, mdOs, mK, mV,
-                    mdQ, p);
-  if (e != cudaSuccess) return e;
-  if (WIN && p.sink_tiles > 0) {
-    const long long st = (long long)p.sink_tiles * p.B * p.G * 2 * kTileB * (p.d / 8);
-    e = launch_kernel(attn_bwd_sink_sum_kernel, dim3((int)((st + 255) / 256)), dim3(256), 0, stream, 1, p);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_kernel(attn_bwd_post_kernel, dim3(blocks), dim3(256), 0, stream, 1, p);
+  return launch_kernel(attn_bwd_post_kernel, dim3((int)((threads + 255) / 256)), dim3(256), 0, stream, 1, p);
 }
 
 cudaError_t launch_attn_bwd(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
                             const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
                             const CUtensorMap& mdQ, const AttnBwdParams& p, cudaStream_t stream) {
-  return launch_bwd<false>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, stream);
-}
-
-cudaError_t launch_attn_bwd_window(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
-                                   const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
-                                   const CUtensorMap& mdQ, const AttnBwdParams& p, cudaStream_t stream) {
-  return launch_bwd<true>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, stream);
+  if (p.d != 64 && p.d != 128) return cudaErrorNotSupported;
+  cudaError_t e = launch_attn_bwd_prep(p, stream);
+  if (e != cudaSuccess) return e;
+  auto kern = p.d == 64 ? attn_bwd_kernel<64> : attn_bwd_kernel<128>;
+  const size_t smem = p.d == 64 ? BwdCfg<64>::Smem : BwdCfg<128>::Smem;
+  e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  const int n_kvt = (p.T + kTileB - 1) / kTileB;
+  e = launch_kernel(kern, dim3(n_kvt * p.B * p.G), dim3(kBwdThreads), smem, stream, 1, mQ, mQs, mdO, mdOs, mK, mV,
+                    mdQ, p);
+  if (e != cudaSuccess) return e;
+  return launch_attn_bwd_post(p, stream);
 }
 
 }  // namespace gqe

@@ -1,0 +1,711 @@
+// attn_bwd_window.cu -- backward of the windowed prefill attention on tcgen05.
+//
+// The mathematics is attn_bwd.cu's (dV = P^T dO, dS = scale * P o (dP - Delta),
+// dK = dS^T q, dq = dS K with P from the forward's log-sum-exp) over the keys a
+// window leaves: query t sees key p when p <= t and (p > t - window or
+// p < sinks).  Key tile j therefore walks the query tiles from token 128 j up to
+// the last token whose window reaches its last key, and to the end when it
+// holds a sink.
+//
+// Under a window the walks are short (window / 128 + 1 query tiles of each kind
+// of row) except the sink tiles', which are as long as the sequence.  One CTA
+// per key tile, as without a window, then spends a third of its time starting
+// and ending (5.5 of 16.6 us at a window of 512, d = 64) and waits for the sink
+// tiles.  Here the walks of all key tiles of all sequences form one list of
+// (key tile, query tile) pairs, cut into equal stretches, one per SM, and each
+// CTA runs its stretch as one pipeline: the loads and products of the next key
+// tile start while the last one's are still running.  A walk cut by a stretch's
+// end leaves its dK, dV sums in fp32 in a slot of its CTA, and
+// attn_bwd_window_join_kernel adds the slots of a walk in their order, so dK
+// and dV do not depend on timing.  dQ goes through TMA reduce-add into fp32 as
+// in attn_bwd.cu.
+//
+// CTA: 512 threads, roles, tensor memory and barriers as in attn_bwd.cu, with
+// every ring counted over the whole stretch.  d = 64 keeps two key tiles' K and
+// V in shared memory; d = 128 has room for one.  Tensor memory holds one dK and
+// one dV: the next key tile's first products into them wait until the drain
+// warps have read them (acc_free).
+//
+// P and dS are computed with packed pairs (f32x2): the prep kernel stores -LSE2
+// and -Delta, so a pair costs one FMA before its exponentials and one add and
+// one multiply after them; the scale of dS moves to where dK and dq are rounded.
+// Exponentials on the FMA-pipe polynomial (2 or 4 of 16 pairs) changed the time
+// by +0.5 and +2.5 %, so all run on MUFU.
+#include "attn.cuh"
+#include "launch.cuh"
+
+namespace gqe {
+
+namespace {
+
+constexpr int kThreadsW = 512;
+constexpr int kTileW = 128;
+constexpr int kBoxW = 128 * 64 * 2;   // one 128-row x 64-column bf16 TMA box
+
+struct __align__(8) BwdWinBarriers {
+  uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
+  uint64_t q_full[2], q_empty[2], o_full[2], o_empty[2];
+  uint64_t s_full, s_free, p_full, pv_done, dp_full, ds_full, dk_done, dq_full, dq_free, acc_free;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+struct BwdWinCfg {
+  static constexpr int NB = D / 64;
+  static constexpr int TileBytes = NB * kBoxW;        // one 128-row tile of Q, dO, K or V
+  static constexpr bool kWide = D == 128;
+  static constexpr int KVB = kWide ? 1 : 2;           // key tiles whose K and V are held
+  static constexpr int OST = kWide ? 1 : 2;           // dO ring depth
+  static constexpr int EpiCh = kWide ? 1 : D / 32;    // 32-column dQ chunks staged per warp at once
+  static constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 256 + D;
+  static constexpr uint32_t kDQ = kWide ? 128 : 384;
+  static constexpr uint32_t kPT = 448;                // d = 64: P^T
+  static constexpr int OffK = 0;
+  static constexpr int OffV = OffK + KVB * TileBytes;
+  static constexpr int OffQ = OffV + KVB * TileBytes;           // [2] stages
+  static constexpr int OffDO = OffQ + 2 * TileBytes;            // [OST]
+  static constexpr int OffDS = OffDO + OST * TileBytes;         // 128 x 128 bf16, MN-major
+  static constexpr int OffEpi = OffDS + 2 * kBoxW;              // 4 warps x EpiCh x 4 KB
+  static constexpr int OffLse = OffEpi + 4 * EpiCh * 4096;      // [2][128] f32
+  static constexpr int OffDelta = OffLse + 2 * 512;             // [2][128] f32
+  static constexpr int OffBar = OffDelta + 2 * 512;
+  static constexpr size_t Smem = 1024 + OffBar + sizeof(BwdWinBarriers);
+  // tensor-memory columns of P^T and dS^T, by 16-query k-step and by warpgroup
+  static __device__ __forceinline__ uint32_t pt_col(int ks) { return kWide ? kS + ks * 8 : kPT + ks * 8; }
+  static __device__ __forceinline__ uint32_t dst_col(int ks) {
+    return kWide ? kS + 64 + ks * 8 : kDP + (ks >> 2) * 64 + (ks & 3) * 8;
+  }
+  static __device__ __forceinline__ uint32_t pt_wcol(int w) { return kWide ? kS + 32 * w : kPT + 32 * w; }
+  static __device__ __forceinline__ uint32_t dst_wcol(int w) { return kWide ? kS + 64 + 32 * w : kDP + 64 * w; }
+};
+
+// Query tiles (routed, then shared) that key tile jt of a group sees.
+__host__ __device__ inline void walk_counts(int T, int k, int window, int sinks, int jt, bool shared, int* n_r,
+                                            int* n_s) {
+  int t_hi = T - 1;                                 // last token that sees a key of the tile
+  if (jt * kTileW >= sinks) {
+    const int reach = jt * kTileW + kTileW - 2 + window;
+    if (reach < t_hi) t_hi = reach;
+  }
+  *n_r = (int)((unsigned)((t_hi + 1) * k + kTileW - 1) / kTileW) - jt * k;
+  *n_s = shared ? (int)((unsigned)t_hi / kTileW) + 1 - jt : 0;
+}
+
+// Position in a CTA's stretch: query tile n of the piece [off, off + cnt) of key
+// tile jt's walk.
+struct Stretch {
+  int left;          // query tiles of the stretch from this piece on
+  int s, b, g;       // KV sequence, its batch entry and its group
+  int jt, off;       // key tile, first query tile of the piece
+  int n_r, total;    // routed query tiles and all query tiles of the whole walk
+  int cnt, n;        // query tiles of the piece, position in it
+  int item;          // pieces before this one
+
+  __device__ __forceinline__ void open(const AttnBwdParams& p) {
+    int n_s;
+    walk_counts(p.T, p.k, p.window, p.sinks, jt, p.n_shared && g == p.sg, &n_r, &n_s);
+    total = n_r + n_s;
+    cnt = min(total - off, left);
+    n = 0;
+  }
+  __device__ __forceinline__ void start(const AttnBwdParams& p, const AttnBwdSchedule& S) {
+    left = S.count[blockIdx.x];
+    s = S.seq[blockIdx.x];
+    b = s / p.G;
+    g = s - b * p.G;
+    jt = S.jt[blockIdx.x];
+    off = S.off[blockIdx.x];
+    item = 0;
+    open(p);
+  }
+  __device__ __forceinline__ bool next_item(const AttnBwdParams& p) {
+    left -= cnt;
+    if (left <= 0) return false;
+    off = 0;
+    ++item;
+    if (++jt * kTileW >= p.T) {
+      jt = 0;
+      ++s;
+      if (++g == p.G) g = 0, ++b;
+    }
+    open(p);
+    return true;
+  }
+  __device__ __forceinline__ bool next(const AttnBwdParams& p) {
+    if (++n < cnt) return true;
+    return next_item(p);
+  }
+  __device__ __forceinline__ bool first() const { return n == 0; }
+  __device__ __forceinline__ bool last() const { return n == cnt - 1; }
+  __device__ __forceinline__ bool whole() const { return off == 0 && cnt == total; }
+  // the query tile: of the shared head or not, its index, its first row in the padded row space
+  __device__ __forceinline__ bool shared() const { return off + n >= n_r; }
+  __device__ __forceinline__ int qi(const AttnBwdParams& p) const {
+    return shared() ? jt + off + n - n_r : jt * p.k + off + n;
+  }
+  __device__ __forceinline__ int row_pad(const AttnBwdParams& p) const {
+    return shared() ? p.B * p.G * p.rows_pad + b * p.rows_pad_sh + qi(p) * kTileW
+                    : s * p.rows_pad + qi(p) * kTileW;
+  }
+};
+
+// One product's k-steps, unrolled: rolled they save 10 KB of code but issue
+// slower, and the chain S -> P -> dV -> S waits for the issue (train step of 2 x
+// 8192 tokens, d = 128: 4.55 against 3.9 us a tile).
+// Both operands K-major, D wide (S, dP).
+template <int D>
+__device__ __forceinline__ void product_kk(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc) {
+  const uint64_t da = sdesc_sw128(a, 16, 1024), db = sdesc_sw128(b, 16, 1024);
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const uint32_t off = (ks >> 2) * kBoxW + (ks & 3) * 32;
+    umma_ss(acc, sdesc_at(da, off), sdesc_at(db, off), idesc, ks > 0);
+  }
+}
+// A from tensor memory (query k-steps 0-3 at a0, 4-7 at a1, 8 columns each), B
+// MN-major in shared memory (dV, dK).
+__device__ __forceinline__ void product_ts(uint32_t acc, uint32_t a0, uint32_t a1, uint32_t b, uint32_t idesc,
+                                           bool accumulate) {
+  const uint64_t db = sdesc_sw128(b, kBoxW, 1024);
+#pragma unroll
+  for (int ks = 0; ks < kTileW / 16; ++ks)
+    umma_ts(acc, (ks < 4 ? a0 : a1) + (ks & 3) * 8, sdesc_at(db, ks * 2048), idesc, accumulate || ks > 0);
+}
+// Both operands MN-major in shared memory (dQ).
+__device__ __forceinline__ void product_mm(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc) {
+  const uint64_t da = sdesc_sw128(a, kBoxW, 1024), db = sdesc_sw128(b, kBoxW, 1024);
+#pragma unroll
+  for (int ks = 0; ks < kTileW / 16; ++ks)
+    umma_ss(acc, sdesc_at(da, ks * 2048), sdesc_at(db, ks * 2048), idesc, ks > 0);
+}
+
+// One row of a key tile's dK and dV out of tensor memory, then acc_free.  A cut
+// walk's go to its slot in fp32 (slot 0 of the CTA when the piece starts inside
+// the walk, else slot 1), a whole walk's are rounded.
+template <int D>
+__device__ __forceinline__ void read_acc(const Stretch& c, const AttnBwdParams& p, uint32_t tmem_lane, int kv,
+                                         uint64_t* acc_free) {
+  using C = BwdWinCfg<D>;
+  const int kv_pos = c.jt * kTileW + kv;
+  const bool whole = c.whole();
+  float* slot = p.part + ((size_t)(2 * blockIdx.x + (c.off > 0 ? 0 : 1)) * 2 * kTileW + kv) * D;
+  const size_t orow = ((size_t)c.s * p.T + kv_pos) * D;
+#pragma unroll 1
+  for (int c0 = 0; c0 < 2 * D; c0 += 32) {       // dK's columns, then dV's
+    const bool dv = c0 >= D;
+    const int col = dv ? c0 - D : c0;
+    uint32_t v[32];
+    tmem_ld32(tmem_lane + (dv ? C::kDV : C::kDK) + col, v);
+    if (c0 == 2 * D - 32) {
+      tc_fence_before();
+      mbar_arrive(acc_free);
+    }
+    if (!whole) {
+      uint4* d4 = reinterpret_cast<uint4*>(slot + (dv ? (size_t)kTileW * D : 0) + col);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d4[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else if (kv_pos < p.T) {
+      const float f = dv ? 1.f : p.scale;
+      uint4* d4 = reinterpret_cast<uint4*>((dv ? p.dV : p.dK) + orow + col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * e]) * f, __uint_as_float(v[8 * i + 2 * e + 1]) * f);
+        d4[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsW, 1)
+attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapQs,
+                       const __grid_constant__ CUtensorMap mapdO, const __grid_constant__ CUtensorMap mapdOs,
+                       const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                       const __grid_constant__ CUtensorMap mapdQ, const __grid_constant__ AttnBwdParams p,
+                       const __grid_constant__ AttnBwdSchedule sched) {
+  using C = BwdWinCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sDS = smem + C::OffDS;
+  float* sLse = reinterpret_cast<float*>(smem + C::OffLse);
+  float* sDelta = reinterpret_cast<float*>(smem + C::OffDelta);
+  BwdWinBarriers* bar = reinterpret_cast<BwdWinBarriers*>(smem + C::OffBar);
+  volatile int* abort = &bar->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto wait = [&](uint64_t* b, uint32_t parity) { return mbar_wait_short(b, parity & 1, abort); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->k_full[i], 1);
+      mbar_init(&bar->v_full[i], 1);
+      mbar_init(&bar->k_empty[i], 2);        // the last S and the last dQ of the key tile
+      mbar_init(&bar->v_empty[i], 1);        // the last dP
+      mbar_init(&bar->q_full[i], 1);
+      mbar_init(&bar->q_empty[i], 2 + 256);
+      mbar_init(&bar->o_full[i], 1);
+      mbar_init(&bar->o_empty[i], 1);
+    }
+    mbar_init(&bar->s_full, 1);
+    mbar_init(&bar->s_free, 256);
+    mbar_init(&bar->p_full, 256);
+    mbar_init(&bar->pv_done, 1);
+    mbar_init(&bar->dp_full, 1);
+    mbar_init(&bar->ds_full, 256);
+    mbar_init(&bar->dk_done, 1);
+    mbar_init(&bar->dq_full, 1);
+    mbar_init(&bar->dq_free, 128);
+    mbar_init(&bar->acc_free, 128);
+    bar->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mapQ);
+    tma_prefetch_desc(&mapdO);
+    tma_prefetch_desc(&mapK);
+    tma_prefetch_desc(&mapV);
+    tma_prefetch_desc(&mapdQ);
+  }
+  if (warp == 1) tmem_alloc(&bar->tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  Stretch c;
+  c.start(p, sched);
+
+  // registers per thread: 96 x 128 + 144 x 256 + 128 x 128 = the launch's 512 x 128
+  if (warp < 4) {
+    set_regs_down<96>();
+    auto wait_w = [&](uint64_t* b, uint32_t parity) { return mbar_wait_warp(b, parity & 1, abort); };
+    const bool leader = elect_one();
+    if (warp == 0) {
+      // ---------------- producer: K, V of each key tile; Q, dO, -LSE2, -Delta of each query tile
+      uint32_t N = 0;
+      do {
+        if (c.first()) {
+          const int b = c.item % C::KVB;
+          const uint32_t ph = c.item / C::KVB - 1;
+          if (c.item >= C::KVB && !wait_w(&bar->k_empty[b], ph)) break;
+          if (leader) {
+            mbar_arrive_expect_tx(&bar->k_full[b], C::TileBytes);
+            for (int bx = 0; bx < C::NB; ++bx)
+              tma_load_3d(smem + C::OffK + b * C::TileBytes + bx * kBoxW, &mapK, &bar->k_full[b], bx * 64, c.jt * kTileW,
+                          c.s);
+          }
+          if (c.item >= C::KVB && !wait_w(&bar->v_empty[b], ph)) break;
+          if (leader) {
+            mbar_arrive_expect_tx(&bar->v_full[b], C::TileBytes);
+            for (int bx = 0; bx < C::NB; ++bx)
+              tma_load_3d(smem + C::OffV + b * C::TileBytes + bx * kBoxW, &mapV, &bar->v_full[b], bx * 64, c.jt * kTileW,
+                          c.s);
+          }
+        }
+        const int st = N & 1, so = N % C::OST;
+        const bool shr = c.shared();
+        const CUtensorMap* mq = shr ? &mapQs : &mapQ;
+        const CUtensorMap* mo = shr ? &mapdOs : &mapdO;
+        const int seq = shr ? c.b : c.s, row = c.qi(p) * kTileW, rp = c.row_pad(p);
+        if (N >= 2 && !wait_w(&bar->q_empty[st], (N >> 1) - 1)) break;
+        if (leader) {
+          mbar_arrive_expect_tx(&bar->q_full[st], C::TileBytes + 2 * 512);
+          for (int bx = 0; bx < C::NB; ++bx)
+            tma_load_3d(smem + C::OffQ + st * C::TileBytes + bx * kBoxW, mq, &bar->q_full[st], bx * 64, row, seq);
+          bulk_load(sLse + st * 128, p.lse2 + rp, 512, &bar->q_full[st]);
+          bulk_load(sDelta + st * 128, p.delta + rp, 512, &bar->q_full[st]);
+        }
+        if (N >= C::OST && !wait_w(&bar->o_empty[so], N / C::OST - 1)) break;
+        if (leader) {
+          mbar_arrive_expect_tx(&bar->o_full[so], C::TileBytes);
+          for (int bx = 0; bx < C::NB; ++bx)
+            tma_load_3d(smem + C::OffDO + so * C::TileBytes + bx * kBoxW, mo, &bar->o_full[so], bx * 64, row, seq);
+        }
+        ++N;
+      } while (c.next(p));
+    } else if (warp == 1) {
+      // ---------------- MMA issuer A: S^T, dP^T, dV
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kTileW, kTileW, false, false);
+      constexpr uint32_t idesc_v = idesc_bf16_f32(kTileW, D, false, true);
+      auto issue_s = [&](const Stretch& t, uint32_t N) {
+        const int st = N & 1, b = t.item % C::KVB;
+        if (t.first() && !wait_w(&bar->k_full[b], t.item / C::KVB)) return false;
+        if (!wait_w(&bar->q_full[st], N >> 1)) return false;
+        tc_fence_after();
+        if (leader) {
+          product_kk<D>(tmem + C::kS, smem_u32(smem + C::OffK + b * C::TileBytes),
+                        smem_u32(smem + C::OffQ + st * C::TileBytes), idesc_s);
+          umma_commit(&bar->s_full);
+          if (t.last()) umma_commit(&bar->k_empty[b]);
+        }
+        return true;
+      };
+      // nx is query tile N + 1, c query tile N (the first round has none)
+      Stretch nx = c;
+      bool more = true;
+      for (uint32_t N = 0xFFFFFFFFu;; ++N) {
+        const bool none = N == 0xFFFFFFFFu;
+        // d = 64: S^T(N+1) as soon as the warpgroups hold S^T(N) in registers
+        if (!C::kWide && more) {
+          if (!none && !wait_w(&bar->s_free, N)) break;
+          if (!issue_s(nx, N + 1)) break;
+        }
+        if (!none) {
+          // dV += P^T dO_i once P^T is in tensor memory (and, at a key tile's
+          // first query tile, the last key tile's dV has been read)
+          if (!wait_w(&bar->p_full, N)) break;
+          if (c.first() && c.item > 0 && !wait_w(&bar->acc_free, c.item - 1)) break;
+          tc_fence_after();
+          if (leader) {
+            product_ts(tmem + C::kDV, tmem + C::pt_col(0), tmem + C::pt_col(4),
+                       smem_u32(smem + C::OffDO + (N % C::OST) * C::TileBytes), idesc_v, !c.first());
+            umma_commit(&bar->pv_done);
+            umma_commit(&bar->q_empty[N & 1]);
+            umma_commit(&bar->o_empty[N % C::OST]);
+          }
+          if (!more) break;
+          // d = 64: dP^T(N+1) overwrites dS^T(N).  d = 128: S^T(N+1) overwrites
+          // P^T(N) and dS^T(N), dP^T(N+1) overwrites dQ(N)
+          if (C::kWide && !wait_w(&bar->pv_done, N)) break;
+          if (!wait_w(&bar->dk_done, N)) break;
+        }
+        if (C::kWide) {
+          if (!issue_s(nx, N + 1)) break;
+          if (!none && !wait_w(&bar->dq_free, N)) break;
+        }
+        const int so = (N + 1) % C::OST, b = nx.item % C::KVB;
+        if (nx.first() && !wait_w(&bar->v_full[b], nx.item / C::KVB)) break;
+        if (!wait_w(&bar->o_full[so], (N + 1) / C::OST)) break;
+        tc_fence_after();
+        if (leader) {
+          product_kk<D>(tmem + C::kDP, smem_u32(smem + C::OffV + b * C::TileBytes),
+                        smem_u32(smem + C::OffDO + so * C::TileBytes), idesc_s);
+          umma_commit(&bar->dp_full);
+          if (nx.last()) umma_commit(&bar->v_empty[b]);
+        }
+        c = nx;
+        more = nx.next(p);
+      }
+    } else if (warp == 2) {
+      // ---------------- MMA issuer B: dK += dS^T Q_i, dQ_i = dS K_j
+      constexpr uint32_t idesc_k = idesc_bf16_f32(kTileW, D, false, true);
+      constexpr uint32_t idesc_q = idesc_bf16_f32(kTileW, D, true, true);
+      uint32_t N = 0;
+      do {
+        const int b = c.item % C::KVB;
+        if (!wait_w(&bar->ds_full, N)) break;
+        if (c.first() && c.item > 0 && !wait_w(&bar->acc_free, c.item - 1)) break;
+        tc_fence_after();
+        if (leader) {
+          product_ts(tmem + C::kDK, tmem + C::dst_col(0), tmem + C::dst_col(4),
+                     smem_u32(smem + C::OffQ + (N & 1) * C::TileBytes), idesc_k, !c.first());
+          umma_commit(&bar->q_empty[N & 1]);
+          umma_commit(&bar->dk_done);      // dS^T(N) has been read from tensor memory
+        }
+        // dQ(N) over dQ(N-1): wait for its drain (d = 128: dQ sits over dP^T's
+        // columns, which the warpgroups have read, ds_full)
+        if (!C::kWide && N >= 1 && !wait_w(&bar->dq_free, N - 1)) break;
+        tc_fence_after();
+        if (leader) {
+          product_mm(tmem + C::kDQ, smem_u32(sDS), smem_u32(smem + C::OffK + b * C::TileBytes), idesc_q);
+          umma_commit(&bar->dq_full);
+          if (c.last()) umma_commit(&bar->k_empty[b]);
+        }
+        ++N;
+      } while (c.next(p));
+    }
+  } else if (warp < 12) {
+    set_regs_up<144>();
+    // ---------------- P and dS: one key row per thread, 64 query columns per warpgroup
+    const int wg = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t col0 = (uint32_t)(wg * 64);
+    const unsigned long long sl2x2 = f2_pack(p.scale_log2, p.scale_log2);
+    uint32_t N = 0;
+    do {
+      const int st = N & 1;
+      const int kv_pos = c.jt * kTileW + r, kk = c.shared() ? 1 : p.k, base = c.qi(p) * kTileW + (int)col0;
+      // query columns c < cmin belong to tokens before this key, c >= cmax to
+      // tokens whose window starts behind it
+      const int cmin = kv_pos * kk - base;
+      const int cmax = kv_pos < p.sinks ? kTileW : (kv_pos + p.window) * kk - base;
+      bool ok = wait(&bar->q_full[st], N >> 1);
+      ok = ok && wait(&bar->s_full, N);
+      if (!C::kWide && !ok) break;
+      tc_fence_after();
+      const float* lse2 = sLse + st * 128 + col0;
+      const float* dlt = sDelta + st * 128 + col0;
+      float pf[64];
+      if (ok) {
+        tmem_ld64(tmem + lane_off + C::kS + col0, reinterpret_cast<uint32_t*>(pf));
+        if (!C::kWide) {
+          tc_fence_before();
+          mbar_arrive(&bar->s_free);      // S^T(N) is in registers
+        }
+#pragma unroll
+        for (int q = 0; q < 64; q += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(lse2 + q);
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(pf[q + e], pf[q + e + 1]), sl2x2, e ? f2_pack(l4.z, l4.w) : f2_pack(l4.x, l4.y)),
+                      x0, x1);
+            pf[q + e] = ex2(x0);
+            pf[q + e + 1] = ex2(x1);
+          }
+        }
+        if (cmin > 0 || cmax < 64) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t vis = ~bits_below(cmin, 32 * h) & bits_below(cmax, 32 * h);
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (!((vis >> q) & 1u)) pf[32 * h + q] = 0.f;
+          }
+        }
+      }
+      if (!C::kWide) {
+        // P^T(N-1) must have been read by dV(N-1) before P^T(N) replaces it
+        if (N > 0 && !wait(&bar->pv_done, N - 1)) break;
+        tc_fence_after();
+      } else {
+        // both warpgroups hold their S^T columns in registers before warpgroup 1
+        // writes P^T over warpgroup 0's; every thread of the two warpgroups
+        // passes here each tile and they leave together if any wait failed
+        int any_fail;
+        asm volatile(
+            "{\n\t.reg .pred q, r;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "bar.red.or.pred r, 1, 256, q;\n\tselp.b32 %0, 1, 0, r;\n\t}"
+            : "=r"(any_fail)
+            : "r"((int)!ok)
+            : "memory");
+        if (any_fail) break;
+      }
+      {
+        uint32_t pk[32];
+#pragma unroll
+        for (int q = 0; q < 32; ++q) pk[q] = pack_bf16x2(pf[2 * q], pf[2 * q + 1]);
+        tmem_st32(tmem + lane_off + C::pt_wcol(wg), pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bar->p_full);
+
+      if (!wait(&bar->dp_full, N)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        uint32_t dp[32], dsk[16];
+        tmem_ld32(tmem + lane_off + C::kDP + col0 + ch * 32, dp);
+#pragma unroll
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const int q = ch * 32 + c4 * 4;
+          const float4 d4 = *reinterpret_cast<const float4*>(dlt + q);
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const unsigned long long t =
+                f2_add(f2_pack(__uint_as_float(dp[c4 * 4 + e]), __uint_as_float(dp[c4 * 4 + e + 1])),
+                       e ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y));
+            float a0, a1;
+            f2_unpack(f2_mul(f2_pack(pf[q + e], pf[q + e + 1]), t), a0, a1);
+            dsk[c4 * 2 + e / 2] = pack_bf16x2(a0, a1);
+          }
+        }
+        // dS^T row r for dK: into this warpgroup's tensor-memory columns ...
+        tmem_st16(tmem + lane_off + C::dst_wcol(wg) + ch * 16, dsk);
+        // ... and for dQ into the MN-major smem operand (the 64-query atom of this
+        // warpgroup, 16-byte pieces swizzled by key row), once dQ(N-1) has read
+        // the previous tile's (d = 128: dP^T(N) was issued after that)
+        if (!C::kWide && ch == 0 && N > 0) ok = wait(&bar->dq_full, N - 1);
+        if (!ok) break;
+        uint8_t* atom = sDS + wg * kBoxW + r * 128;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          st_shared_v4(atom + (((ch * 4 + j) ^ (r & 7)) << 4), dsk[j * 4], dsk[j * 4 + 1], dsk[j * 4 + 2],
+                       dsk[j * 4 + 3]);
+      }
+      if (!ok) break;
+      tmem_wait_st();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&bar->ds_full);
+      mbar_arrive(&bar->q_empty[st]);
+      ++N;
+    } while (c.next(p));
+  } else {
+    // ---------------- dQ drain (TMA reduce-add into fp32); dK, dV at the end of each key tile
+    const int qd = warp & 3;
+    const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+    uint8_t* stage = smem + C::OffEpi + qd * C::EpiCh * 4096;
+    uint32_t N = 0;
+    do {
+      // A key tile's last query tile: dK and dV first at d = 64 (they are done
+      // before dQ is), so that the next key tile's products into them start; at
+      // d = 128 the next dP^T waits for the dQ drain, so that comes first.
+#pragma unroll 1
+      for (int step = 0; step < 2; ++step) {
+      if ((step == 0) != C::kWide) {
+        if (!c.last()) continue;
+        if (!wait(&bar->pv_done, N) || !wait(&bar->dk_done, N)) goto out;
+        tc_fence_after();
+        read_acc<D>(c, p, tmem + lane_off, qd * 32 + lane, &bar->acc_free);
+        continue;
+      }
+      if (!wait(&bar->dq_full, N)) goto out;
+      tc_fence_after();
+      const int row_pad = c.row_pad(p);
+#pragma unroll
+      for (int g0 = 0; g0 < D / 32; g0 += C::EpiCh) {
+        // staging free: every earlier reduce of this warp has read it
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < C::EpiCh; ++i) {
+          uint32_t v[32];
+          tmem_ld32(tmem + lane_off + C::kDQ + (g0 + i) * 32, v);
+          if (g0 + i == D / 32 - 1) {
+            tc_fence_before();
+            mbar_arrive(&bar->dq_free);
+          }
+          uint8_t* rowp = stage + i * 4096 + lane * 128;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            st_shared_v4(rowp + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < C::EpiCh; ++i)
+            tma_reduce_add_2d(&mapdQ, stage + i * 4096, (g0 + i) * 32, row_pad + qd * 32);
+          bulk_commit();
+        }
+      }
+      }
+      ++N;
+    } while (c.next(p));
+  out:
+    if (lane == 0) bulk_wait<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  report_abort(abort, p.err, kErrTimeoutAttnBwd);
+  drain_after_abort(abort);
+}
+
+// dK, dV of the walks that the stretches' ends cut: block c adds the pieces of
+// the walk cut between CTAs c-1 and c, when that is the walk's first cut.
+__global__ void __launch_bounds__(256)
+attn_bwd_window_join_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnBwdSchedule S) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int c = blockIdx.x + 1;
+  const int s = S.seq[c], jt = S.jt[c];
+  if (S.off[c] == 0) return;                                                     // the walk starts here
+  if (S.seq[c - 1] == s && S.jt[c - 1] == jt && S.off[c - 1] > 0) return;         // cut before
+  int last = c;
+  while (last + 1 < S.n_ctas && S.seq[last + 1] == s && S.jt[last + 1] == jt && S.off[last + 1] > 0) ++last;
+  const size_t slot = (size_t)2 * kTileW * p.d;
+  const int per = p.d / 4;
+  for (int e = blockIdx.y * 256 + threadIdx.x; e < 2 * kTileW * per; e += gridDim.y * 256) {
+    const int c4 = e % per, row = e / per % kTileW, which = e / per / kTileW;
+    const int kv_pos = jt * kTileW + row;
+    if (kv_pos >= p.T) continue;
+    const size_t at = ((size_t)which * kTileW + row) * p.d + c4 * 4;
+    float4 a = *reinterpret_cast<const float4*>(p.part + (size_t)(2 * (c - 1) + 1) * slot + at);
+    for (int i = c; i <= last; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(p.part + (size_t)(2 * i) * slot + at);
+      a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    }
+    const float f = which ? 1.f : p.scale;
+    gqe_bf16_t* dst = (which ? p.dV : p.dK) + ((size_t)s * p.T + kv_pos) * p.d;
+    reinterpret_cast<uint2*>(dst)[c4] = make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+  }
+}
+
+}  // namespace
+
+// Walks in the order of the sequences, and of the key tiles in each, cut into
+// stretches of equal length (to within one query tile).
+void attn_bwd_window_plan(int B, int T, int G, int k, int n_shared, int sg, int d, int window, int sinks,
+                          AttnBwdSchedule* S, size_t* off_part, size_t* bytes) {
+  const int n_jt = (T + kTileW - 1) / kTileW;
+  long long plain = 0, extra = 0;      // query tiles of a sequence's walks: routed, and the shared head's
+  for (int j = 0; j < n_jt; ++j) {
+    int r, s;
+    walk_counts(T, k, window, sinks, j, n_shared != 0, &r, &s);
+    plain += r;
+    extra += s;
+  }
+  const long long per_b = plain * G + extra, total = per_b * B;
+  const int n = total < kBwdWindowCtas ? (int)total : kBwdWindowCtas;
+  S->n_ctas = n;
+  int seq = -1, j = 0;
+  long long before = 0;                // query tiles before walk (seq, j)
+  for (int c = 0; c < n; ++c) {
+    const long long at = total * c / n;
+    S->count[c] = (int)(total * (c + 1) / n - at);
+    // the sequence by division, the key tile by walking (on from the last CTA's)
+    const long long b = at / per_b, in_b = at % per_b;
+    long long g, base;
+    if (in_b < plain * sg) g = in_b / plain, base = g * plain;
+    else if (in_b < plain * (sg + 1) + extra) g = sg, base = plain * sg;
+    else g = (in_b - extra) / plain, base = g * plain + extra;
+    if (b * G + g != seq) {
+      seq = (int)(b * G + g);
+      j = 0;
+      before = b * per_b + base;
+    }
+    for (;; ++j) {
+      int r, s;
+      walk_counts(T, k, window, sinks, j, n_shared && g == sg, &r, &s);
+      if (at < before + r + s) break;
+      before += r + s;
+    }
+    S->seq[c] = seq;
+    S->jt[c] = j;
+    S->off[c] = (int)(at - before);
+  }
+  AttnBwdLayout L;
+  attn_bwd_layout(B, T, G, k, n_shared, d, &L);
+  *off_part = (L.bytes + 255) & ~size_t(255);
+  *bytes = *off_part + (size_t)2 * n * 2 * kTileW * d * sizeof(float);
+}
+
+template <int D>
+static cudaError_t launch_win(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
+                              const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
+                              const CUtensorMap& mdQ, const AttnBwdParams& p, const AttnBwdSchedule& S,
+                              cudaStream_t stream) {
+  auto kern = attn_bwd_window_kernel<D>;
+  const size_t smem = BwdWinCfg<D>::Smem;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(S.n_ctas), dim3(kThreadsW), smem, stream, 1, mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S);
+}
+
+cudaError_t launch_attn_bwd_window(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
+                                   const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
+                                   const CUtensorMap& mdQ, const AttnBwdParams& p, const AttnBwdSchedule& S,
+                                   cudaStream_t stream) {
+  cudaError_t e = launch_attn_bwd_prep(p, stream);
+  if (e != cudaSuccess) return e;
+  e = p.d == 64 ? launch_win<64>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S, stream)
+                : launch_win<128>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S, stream);
+  if (e != cudaSuccess) return e;
+  if (S.n_ctas > 1) {
+    e = launch_kernel(attn_bwd_window_join_kernel, dim3(S.n_ctas - 1, 8), dim3(256), 0, stream, 1, p, S);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_attn_bwd_post(p, stream);
+}
+
+}  // namespace gqe

@@ -103,12 +103,6 @@ __device__ __forceinline__ CacheList cache_list(const CacheAttnParams& p, int b)
   return c;
 }
 
-// Bits i of a 32-key word at position pos with pos + i < x.
-__device__ __forceinline__ uint32_t bits_below(int x, int pos) {
-  const int n = min(max(x - pos, 0), 32);
-  return n == 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
-}
-
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t* r) {
   if constexpr (N == 16) tmem_ld16(a, r);
@@ -156,7 +150,7 @@ __device__ __forceinline__ RowState cache_softmax(const CacheAttnParams& p, cons
     const int i = first + j;
     const bool in_tree = i >= cl.n_cache;
     const int kb = cl.row<KT>(i);
-    st.ok = mbar_wait(&sh->s_full, j & 1, abort, p.err, kErrTimeoutCacheAttn);
+    st.ok = mbar_wait_short(&sh->s_full, j & 1, abort);
     tc_fence_after();
     uint32_t s[NC];
     tmem_ld<NC>(s_base, s);
@@ -215,7 +209,7 @@ __device__ __forceinline__ RowState cache_softmax(const CacheAttnParams& p, cons
     st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     if (j > 0) {
       // P(j-1) V must be done before P is overwritten and O rescaled
-      st.ok = mbar_wait(&sh->pv_done, (j - 1) & 1, abort, p.err, kErrTimeoutCacheAttn) && st.ok;
+      st.ok = mbar_wait_short(&sh->pv_done, (j - 1) & 1, abort) && st.ok;
       tc_fence_after();
       if (rescale) {
 #pragma unroll 1
@@ -233,7 +227,7 @@ __device__ __forceinline__ RowState cache_softmax(const CacheAttnParams& p, cons
     const bool dead_keys = in_tree ? kb + KT > cl.m
                                    : kb + KT > cl.len || (p.window && kb < cl.lo0 && kb + KT > p.sinks);
     if (dead_keys) {
-      st.ok = mbar_wait(&sh->v_full[j % C::VST], (j / C::VST) & 1, abort, p.err, kErrTimeoutCacheAttn) && st.ok;
+      st.ok = mbar_wait_short(&sh->v_full[j % C::VST], (j / C::VST) & 1, abort) && st.ok;
       const int r = threadIdx.x, pos = kb + r;
       if (r < KT && (in_tree ? pos >= cl.m : pos >= cl.len || (pos < cl.lo0 && pos >= p.sinks))) {
         uint8_t* row = sV + (j % C::VST) * C::KVBytes + r * 128;
@@ -248,7 +242,7 @@ __device__ __forceinline__ RowState cache_softmax(const CacheAttnParams& p, cons
     tc_fence_before();
     mbar_arrive(&sh->p_full);
   }
-  st.ok = mbar_wait(&sh->pv_done, (n - 1) & 1, abort, p.err, kErrTimeoutCacheAttn) && st.ok;
+  st.ok = mbar_wait_short(&sh->pv_done, (n - 1) & 1, abort) && st.ok;
   tc_fence_after();
   return st;
 }
@@ -512,19 +506,20 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
       bool ok = true;
       for (int j = 0; ok && j < n; ++j) {
         const int s = j % KST;
-        if (j > 0) ok = mbar_wait(&sh->s_free, (j - 1) & 1, abort, p.err, kErrTimeoutCacheAttn);
-        ok = ok && mbar_wait(&sh->k_full[s], (j / KST) & 1, abort, p.err, kErrTimeoutCacheAttn);
+        if (j > 0) ok = mbar_wait_short(&sh->s_free, (j - 1) & 1, abort);
+        ok = ok && mbar_wait_short(&sh->k_full[s], (j / KST) & 1, abort);
         if (!ok) break;
         tc_fence_after();
         const uint32_t k0 = smem_u32(sK + s * C::KVBytes);
+        const uint64_t dq = sdesc_sw128(q0, 16, 1024), dk = sdesc_sw128(k0, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          umma_ss(tmem + C::kS, sdesc_sw128(q0 + (ks >> 2) * C::QBox + (ks & 3) * 32, 16, 1024),
-                  sdesc_sw128(k0 + (ks >> 2) * C::KBox + (ks & 3) * 32, 16, 1024), idesc_s, ks > 0);
+          umma_ss(tmem + C::kS, sdesc_at(dq, (ks >> 2) * C::QBox + (ks & 3) * 32),
+                  sdesc_at(dk, (ks >> 2) * C::KBox + (ks & 3) * 32), idesc_s, ks > 0);
         umma_commit(&sh->s_full);
         umma_commit(&sh->k_empty[s]);
         if (j + KST < n) {
-          ok = mbar_wait(&sh->k_empty[s], (j / KST) & 1, abort, p.err, kErrTimeoutCacheAttn);
+          ok = mbar_wait_short(&sh->k_empty[s], (j / KST) & 1, abort);
           if (!ok) break;
           load_k(j + KST);
         }
@@ -535,18 +530,18 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRowsQ, D, false, true);
       for (int j = 0; j < n; ++j) {
         const int s = j % VST;
-        if (!mbar_wait(&sh->p_full, j & 1, abort, p.err, kErrTimeoutCacheAttn)) break;
-        if (!mbar_wait(&sh->v_full[s], (j / VST) & 1, abort, p.err, kErrTimeoutCacheAttn)) break;
+        if (!mbar_wait_short(&sh->p_full, j & 1, abort)) break;
+        if (!mbar_wait_short(&sh->v_full[s], (j / VST) & 1, abort)) break;
         tc_fence_after();
         const uint32_t v0 = smem_u32(sV + s * C::KVBytes);
+        const uint64_t dv = sdesc_sw128(v0, C::KBox, 1024);
 #pragma unroll
         for (int ks = 0; ks < KT / 16; ++ks)
-          umma_ts(tmem + C::kO, tmem + C::kP + ks * 8, sdesc_sw128(v0 + ks * 2048, C::KBox, 1024), idesc_o,
-                  (j > 0 || ks > 0));
+          umma_ts(tmem + C::kO, tmem + C::kP + ks * 8, sdesc_at(dv, ks * 2048), idesc_o, (j > 0 || ks > 0));
         umma_commit(&sh->pv_done);
         umma_commit(&sh->v_empty[s]);
         if (j + VST < n) {
-          if (!mbar_wait(&sh->v_empty[s], (j / VST) & 1, abort, p.err, kErrTimeoutCacheAttn)) break;
+          if (!mbar_wait_short(&sh->v_empty[s], (j / VST) & 1, abort)) break;
           load_v(j + VST);
         }
       }
@@ -615,6 +610,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     tmem_dealloc(tmem, 256);
   }
   join_shares<D>(p, sh, smem, bg, row0, n_rows, kr);
+  report_abort(abort, p.err, kErrTimeoutCacheAttn);
   drain_after_abort(abort);
 }
 

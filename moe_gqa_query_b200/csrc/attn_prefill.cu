@@ -31,14 +31,6 @@
 //   d=64 : S_A 0 | S_B 128 | O_A 256 | O_B 320 | P_A 384 | P_B 448
 //   d=128: S_A 0 | S_B 128 | O_A 256 | O_B 384, P_X written over S_X's first
 //          64 columns (the next S_X waits for P_X V to finish).
-//
-// Sliding window with sinks (WIN instances): query t sees key p when p <= t and
-// (p > t - window or p < sinks).  A query tile then walks a list of key tiles
-// instead of the prefix: the tiles that hold sinks, and the tiles from its
-// first row's window start on.  Masks are applied on the tiles that hold a
-// border of the visible set.  A row may see nothing of a tile (its window
-// starts behind it): its running max stays -inf, its exponentials are taken
-// against 0 and come out 0.
 #include "attn.cuh"
 #include "launch.cuh"
 
@@ -125,42 +117,7 @@ __device__ __forceinline__ TileInfo tile_info(int qt, int rows_total, int kk, in
   return ti;
 }
 
-// The key tiles a query tile walks under a window: sink tiles 0 .. n_sink-1,
-// then w0, w0+1, ... up to the tile of its last token.
-struct KeyList {
-  int n, n_sink, w0;
-  __device__ __forceinline__ int tile(int j) const { return j < n_sink ? j : w0 + j - n_sink; }
-};
-
-__device__ __forceinline__ int first_window_tile(int t_first, int window) {
-  return max(0, t_first - window + 1) / kTile;
-}
-
-// n_end: one past the last key tile, w0: the first tile of the window.
-__device__ __forceinline__ KeyList key_list(int w0, int n_end, int sinks) {
-  KeyList l;
-  l.w0 = w0;
-  l.n_sink = min((sinks + kTile - 1) / kTile, w0);
-  l.n = l.n_sink + n_end - w0;
-  return l;
-}
-
-// Masks the keys of tile jt that the row of token t_r does not see under the
-// window: columns [sinks - base, t_r - window + 1 - base) of the tile at base.
-__device__ __forceinline__ void mask_window(uint32_t (&s)[128], int t_r, int jt, int window, int sinks) {
-  const int lo = t_r - window + 1 - jt * kTile, sk = sinks - jt * kTile;
-#pragma unroll
-  for (int c = 0; c < 128; ++c)
-    if (c < lo && c >= sk) s[c] = __float_as_uint(-INFINITY);
-}
-
-// Whether tile jt holds a key that some row up to token t_last does not see
-// because its window starts behind it.
-__device__ __forceinline__ bool window_border(int t_last, int jt, int window, int sinks) {
-  return jt * kTile < t_last - window + 1 && jt * kTile + kTile > sinks;
-}
-
-template <int D, bool WIN>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapQs,
                     const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
@@ -202,30 +159,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
   const TileInfo tA = tile_info(2 * pair, rows_total, kk, p.T);
   const TileInfo tB = tile_info(2 * pair + 1, rows_total, kk, p.T);
   if (tA.n_kv == 0) return;
-  // Key tiles of the pair.  Under a window the two tiles share one list, from
-  // tile A's window start to the last key tile of either; tile B skips the
-  // entries [gap, gap + gap_n) that lie before its own window and hold no sink.
-  KeyList kl{max(tA.n_kv, tB.n_kv), 0, 0};
-  int gap = 0, gap_n = 0, nA = tA.n_kv, nB = tB.n_kv;
-  if (WIN) {
-    const int sink_tiles = (p.sinks + kTile - 1) / kTile;
-    const int wA = first_window_tile(tA.t_first, p.window);
-    kl = key_list(wA, max(tA.n_kv, tB.n_kv), p.sinks);
-    nA = kl.n_sink + tA.n_kv - wA;
-    if (nB > 0) {
-      nB = kl.n;
-      const int g0 = max(wA, sink_tiles);
-      gap = kl.n_sink + g0 - wA;
-      gap_n = max(0, first_window_tile(tB.t_first, p.window) - g0);
-    }
-  }
-  const int n_kv = kl.n;
-  // whether tile x (0: A, 1: B) uses list entry j, and how many it used before
-  auto active = [&](int x, int j) {
-    if (!WIN) return j < (x ? nB : nA);
-    return x ? j < nB && (j < gap || j >= gap + gap_n) : j < nA;
-  };
-  auto used = [&](int x, int j) { return WIN && x && j >= gap ? j - gap_n : j; };
+  const int n_kv = max(tA.n_kv, tB.n_kv);
   const CUtensorMap* mq = routed ? &mapQ : &mapQs;
 
   if (threadIdx.x == 0) {
@@ -264,16 +198,16 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
         for (int bx = 0; bx < C::NB; ++bx)
           tma_load_3d(sQ + x * C::QBytes + bx * kBox, mq, &bar->q_full, bx * 64, (x ? tB : tA).row0, seq);
       for (int j = 0; j < n_kv; ++j) {
-        const int s = j % C::ST, jt = kl.tile(j);
+        const int s = j % C::ST;
         const uint32_t ph = ((j / C::ST) & 1) ^ 1;
         if (j >= C::ST && !mbar_wait(&bar->k_empty[s], ph, abort, p.err, kErrTimeoutAttn)) break;
         mbar_arrive_expect_tx(&bar->k_full[s], C::KVBytes);
         for (int bx = 0; bx < C::NB; ++bx)
-          tma_load_3d(sK + s * C::KVBytes + bx * kBox, &mapK, &bar->k_full[s], bx * 64, jt * kTile, kvseq);
+          tma_load_3d(sK + s * C::KVBytes + bx * kBox, &mapK, &bar->k_full[s], bx * 64, j * kTile, kvseq);
         if (j >= C::ST && !mbar_wait(&bar->v_empty[s], ph, abort, p.err, kErrTimeoutAttn)) break;
         mbar_arrive_expect_tx(&bar->v_full[s], C::KVBytes);
         for (int bx = 0; bx < C::NB; ++bx)
-          tma_load_3d(sV + s * C::KVBytes + bx * kBox, &mapV, &bar->v_full[s], bx * 64, jt * kTile, kvseq);
+          tma_load_3d(sV + s * C::KVBytes + bx * kBox, &mapV, &bar->v_full[s], bx * 64, j * kTile, kvseq);
       }
     }
   } else if (warp == 9) {
@@ -281,6 +215,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
       // ---------------- MMA issuer
       constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, false, false);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, D, false, true);
+      const int nA = tA.n_kv, nB = tB.n_kv;
       bool ok = true;
       auto issue_s = [&](int x, int j) {
         const int s = j % C::ST;
@@ -296,7 +231,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
         }
         umma_commit(&bar->s_full[x]);
         // K_j's last reader is tile B when it reaches j, else tile A
-        if (x == 1 || !active(1, j)) umma_commit(&bar->k_empty[s]);
+        if (x == 1 || nB <= j) umma_commit(&bar->k_empty[s]);
         return true;
       };
       auto issue_pv = [&](int x, int j) {
@@ -307,24 +242,23 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
 #pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks)
           umma_ts(tmem + C::ocol(x), tmem + C::pcol(x) + ks * 8, sdesc_sw128(v0 + ks * 2048, kBox, 1024),
-                  idesc_o, (used(x, j) > 0 || ks > 0));
+                  idesc_o, (j > 0 || ks > 0));
         umma_commit(&bar->pv_done[x]);
-        if (x == 1 || !active(1, j)) umma_commit(&bar->v_empty[s]);
+        if (x == 1 || nB <= j) umma_commit(&bar->v_empty[s]);
         return true;
       };
       if (mbar_wait(&bar->q_full, 0, abort, p.err, kErrTimeoutAttn)) {
         ok = issue_s(0, 0);
-        if (ok && active(1, 0)) ok = issue_s(1, 0);
+        if (ok && nB > 0) ok = issue_s(1, 0);
         for (int j = 0; ok && j < n_kv; ++j) {
           for (int x = 0; x < 2 && ok; ++x) {
-            if (active(x, j)) {
-              ok = mbar_wait(&bar->p_full[x], used(x, j) & 1, abort, p.err, kErrTimeoutAttn);
-              tc_fence_after();
-              ok = ok && issue_pv(x, j);
-            }
-            if (ok && active(x, j + 1)) {
-              const int u = used(x, j + 1);    // 0: tile B's first entry, behind a gap at the front
-              if (C::kPAliasS && u > 0) ok = mbar_wait(&bar->pv_done[x], (u - 1) & 1, abort, p.err, kErrTimeoutAttn);
+            const int nx = x ? nB : nA;
+            if (j >= nx) continue;
+            ok = mbar_wait(&bar->p_full[x], j & 1, abort, p.err, kErrTimeoutAttn);
+            tc_fence_after();
+            ok = ok && issue_pv(x, j);
+            if (ok && j + 1 < nx) {
+              if (C::kPAliasS) ok = mbar_wait(&bar->pv_done[x], j & 1, abort, p.err, kErrTimeoutAttn);
               ok = ok && issue_s(x, j + 1);
             }
           }
@@ -346,18 +280,13 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
       const uint32_t p_base = tmem + lane_off + C::pcol(x);
       const uint32_t o_base = tmem + lane_off + C::ocol(x);
       const float sl2 = p.scale_log2;
-      const int t_last = min(p.T - 1, (ti.row0 + kTile - 1) / kk);
       float m_run = -INFINITY, l_run = 0.f;
       bool ok = true;
-      const int n_x = x ? nB : nA;
-      int n_used = 0;                        // tiles this query tile has worked on
-      for (int e = 0; e < n_x && ok; ++e) {
-        if (!active(x, e)) continue;
-        const int j = n_used++, jt = kl.tile(e);
+      for (int j = 0; j < ti.n_kv && ok; ++j) {
         ok = mbar_wait(&bar->s_full[x], j & 1, abort, p.err, kErrTimeoutAttn);
         tc_fence_after();
-        const bool diag = jt * kTile + kTile - 1 > ti.t_first;
-        const int lim = t_r - jt * kTile;    // columns > lim are in the future
+        const bool diag = j * kTile + kTile - 1 > ti.t_first;
+        const int lim = t_r - j * kTile;     // columns > lim are in the future
         // the whole S row, once (two loads, one wait), then the row max with
         // 8 independent partial maxima
         uint32_t s[128];
@@ -367,7 +296,6 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
           for (int c = 0; c < 128; ++c)
             if (c > lim) s[c] = __float_as_uint(-INFINITY);
         }
-        if (WIN && window_border(t_last, jt, p.window, p.sinks)) mask_window(s, t_r, jt, p.window, p.sinks);
         float m8[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) m8[q] = -INFINITY;
@@ -395,7 +323,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
         }
         // exponentials (MUFU, or the FMA-pipe polynomial for kPolyPairs of every
         // 16 pairs), row sum, P (bf16) into tensor memory
-        const float neg_m = (WIN && m_run == -INFINITY) ? 0.f : -m_run;
+        const float neg_m = -m_run;
         float sum4[4] = {0.f, 0.f, 0.f, 0.f};   // independent partial sums
 #pragma unroll
         for (int c0 = 0; c0 < 64; c0 += 16) {
@@ -437,7 +365,7 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
         mbar_arrive(&bar->p_full[x]);
       }
       // ---------------- epilogue: O / l -> bf16
-      ok = mbar_wait(&bar->pv_done[x], (n_used - 1) & 1, abort, p.err, kErrTimeoutAttn) && ok;
+      ok = mbar_wait(&bar->pv_done[x], (ti.n_kv - 1) & 1, abort, p.err, kErrTimeoutAttn) && ok;
       tc_fence_after();
       const float inv_l = 1.f / l_run;
       gqe_bf16_t* orow = routed ? p.o_routed + ((size_t)seq * rows_total + prow) * D
@@ -499,7 +427,7 @@ struct __align__(8) Attn1Barriers {
 constexpr int kSingleST = 2;   // two CTAs per SM must fit in 228 KB of shared memory
 constexpr size_t kSingleSmem = 1024 + kBox + 2 * kSingleST * kBox + sizeof(Attn1Barriers);
 
-template <int POLY, bool WIN>
+template <int POLY>
 __global__ void __launch_bounds__(192, 2)
 attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapQs,
                            const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
@@ -544,9 +472,7 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
   }
   const TileInfo ti = tile_info(qt, rows_total, kk, p.T);
   if (ti.n_kv == 0) return;
-  const KeyList kl = WIN ? key_list(first_window_tile(ti.t_first, p.window), ti.n_kv, p.sinks)
-                         : KeyList{ti.n_kv, 0, 0};
-  const int n_kv = kl.n;
+  const int n_kv = ti.n_kv;
   const CUtensorMap* mq = routed ? &mapQ : &mapQs;
 
   // The K-side thread sets up the barriers and puts Q and the first K and V
@@ -572,9 +498,9 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
     tma_load_3d(sQ, mq, &bar->q_full, 0, ti.row0, seq);
     for (int j = 0; j < ST && j < n_kv; ++j) {
       mbar_arrive_expect_tx(&bar->k_full[j], kBox);
-      tma_load_3d(sK + j * kBox, &mapK, &bar->k_full[j], 0, kl.tile(j) * kTile, kvseq);
+      tma_load_3d(sK + j * kBox, &mapK, &bar->k_full[j], 0, j * kTile, kvseq);
       mbar_arrive_expect_tx(&bar->v_full[j], kBox);
-      tma_load_3d(sV + j * kBox, &mapV, &bar->v_full[j], 0, kl.tile(j) * kTile, kvseq);
+      tma_load_3d(sV + j * kBox, &mapV, &bar->v_full[j], 0, j * kTile, kvseq);
     }
   }
   if (warp == 5) tmem_alloc(&bar->tmem_base, 256);
@@ -619,7 +545,7 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
           ok = mbar_wait(&bar->k_empty[s], (j / ST) & 1, abort, p.err, kErrTimeoutAttn);
           if (!ok) break;
           mbar_arrive_expect_tx(&bar->k_full[s], kBox);
-          tma_load_3d(sK + s * kBox, &mapK, &bar->k_full[s], 0, kl.tile(j + ST) * kTile, kvseq);
+          tma_load_3d(sK + s * kBox, &mapK, &bar->k_full[s], 0, (j + ST) * kTile, kvseq);
         }
       }
     }
@@ -655,7 +581,7 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
           ok = mbar_wait(&bar->v_empty[s], (j / ST) & 1, abort, p.err, kErrTimeoutAttn);
           if (!ok) break;
           mbar_arrive_expect_tx(&bar->v_full[s], kBox);
-          tma_load_3d(sV + s * kBox, &mapV, &bar->v_full[s], 0, kl.tile(j + ST) * kTile, kvseq);
+          tma_load_3d(sV + s * kBox, &mapV, &bar->v_full[s], 0, (j + ST) * kTile, kvseq);
         }
       }
     }
@@ -671,7 +597,6 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
     const uint32_t p_base = tmem + lane_off + kP;
     const uint32_t o_base = tmem + lane_off + kO;
     const float sl2 = p.scale_log2;
-    const int t_last = min(p.T - 1, (ti.row0 + kTile - 1) / kk);
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < n_kv && ok; ++j) {
@@ -683,9 +608,8 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
         else tr_ws += tw1 - tw0;
       })
       tc_fence_after();
-      const int jt = kl.tile(j);
-      const bool diag = jt * kTile + kTile - 1 > ti.t_first;
-      const int lim = t_r - jt * kTile;
+      const bool diag = j * kTile + kTile - 1 > ti.t_first;
+      const int lim = t_r - j * kTile;
       uint32_t s[128];
       tmem_ld128(s_base, s);
       tc_fence_before();
@@ -695,7 +619,6 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
         for (int c = 0; c < 128; ++c)
           if (c > lim) s[c] = __float_as_uint(-INFINITY);
       }
-      if (WIN && window_border(t_last, jt, p.window, p.sinks)) mask_window(s, t_r, jt, p.window, p.sinks);
       float m8[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) m8[q] = -INFINITY;
@@ -718,7 +641,7 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
           m_run = m_new;
         }
       }
-      const float neg_m = (WIN && m_run == -INFINITY) ? 0.f : -m_run;
+      const float neg_m = -m_run;
 #if GQE_ATTN1_F2
       const unsigned long long sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(neg_m, neg_m);
       unsigned long long sum2[2] = {0ull, 0ull};
@@ -839,11 +762,11 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
 
 }  // namespace
 
-template <int D, bool WIN>
+template <int D>
 static cudaError_t launch_d(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
                             const CUtensorMap& mV, const AttnParams& p, cudaStream_t stream) {
   const size_t smem = AttnCfg<D>::Smem;
-  auto kern = attn_prefill_kernel<D, WIN>;
+  auto kern = attn_prefill_kernel<D>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int n_levels = (p.T + 2 * kTile - 1) / (2 * kTile);
@@ -851,12 +774,9 @@ static cudaError_t launch_d(const CUtensorMap& mQ, const CUtensorMap& mQs, const
   return launch_kernel(kern, dim3(n_levels * per_level), dim3(kThreads), smem, stream, 1, mQ, mQs, mK, mV, p);
 }
 
-template <bool WIN>
 static cudaError_t launch_single(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
                                  const CUtensorMap& mV, const AttnParams& p, cudaStream_t stream) {
-  // under a window every walk is short: the short-walk instance
-  auto kern = !WIN && p.T >= kPolyLongFromT ? attn_prefill_single_kernel<kPolyLongT, false>
-                                            : attn_prefill_single_kernel<kPolyShortT, WIN>;
+  auto kern = p.T >= kPolyLongFromT ? attn_prefill_single_kernel<kPolyLongT> : attn_prefill_single_kernel<kPolyShortT>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), kSingleSmem);
   if (e != cudaSuccess) return e;
   const int n_levels = (p.T + kTile - 1) / kTile;
@@ -867,16 +787,10 @@ static cudaError_t launch_single(const CUtensorMap& mQ, const CUtensorMap& mQs, 
 cudaError_t launch_attn_prefill(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
                                 const CUtensorMap& mV, const AttnParams& p, int d, cudaStream_t stream) {
 #ifndef GQE_ATTN_PAIRED_D64
-  if (d == 64) return launch_single<false>(mQ, mQs, mK, mV, p, stream);
+  if (d == 64) return launch_single(mQ, mQs, mK, mV, p, stream);
 #endif
-  if (d == 64) return launch_d<64, false>(mQ, mQs, mK, mV, p, stream);
-  return launch_d<128, false>(mQ, mQs, mK, mV, p, stream);
-}
-
-cudaError_t launch_attn_prefill_window(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
-                                       const CUtensorMap& mV, const AttnParams& p, int d, cudaStream_t stream) {
-  if (d == 64) return launch_single<true>(mQ, mQs, mK, mV, p, stream);
-  return launch_d<128, true>(mQ, mQs, mK, mV, p, stream);
+  if (d == 64) return launch_d<64>(mQ, mQs, mK, mV, p, stream);
+  return launch_d<128>(mQ, mQs, mK, mV, p, stream);
 }
 
 }  // namespace gqe

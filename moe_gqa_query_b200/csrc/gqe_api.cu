@@ -439,8 +439,10 @@ static gqe_status prefill_common(const gqe_dims* dims, const gqe_bf16* q_routed,
   GQE_REQUIRE(map3d(&mQ, q_routed, d, (uint64_t)T * k, (uint64_t)B * G, 128), GQE_ERR_CUDA);
   if (dims->n_shared) GQE_REQUIRE(map3d(&mQs, q_sh, d, T, B, 128), GQE_ERR_CUDA);
   else mQs = mQ;
-  GQE_REQUIRE(map3d(&mK, K, d, T, (uint64_t)B * G, 128), GQE_ERR_CUDA);
-  GQE_REQUIRE(map3d(&mV, V, d, T, (uint64_t)B * G, 128), GQE_ERR_CUDA);
+  const bool win = has_window(dims, window);
+  const uint32_t box = win ? attn_window_key_tile(d) : 128;
+  GQE_REQUIRE(map3d(&mK, K, d, T, (uint64_t)B * G, box), GQE_ERR_CUDA);
+  GQE_REQUIRE(map3d(&mV, V, d, T, (uint64_t)B * G, box), GQE_ERR_CUDA);
   AttnParams p{};
   p.o_routed = o_routed;
   p.o_sh = o_sh;
@@ -453,7 +455,7 @@ static gqe_status prefill_common(const gqe_dims* dims, const gqe_bf16* q_routed,
   p.sg = dims->shared_kv_group;
   p.scale_log2 = scale_log2(dims);
   p.err = error_word();
-  if (!has_window(dims, window)) return cuda_status(launch_attn_prefill(mQ, mQs, mK, mV, p, d, S(stream)));
+  if (!win) return cuda_status(launch_attn_prefill(mQ, mQs, mK, mV, p, d, S(stream)));
   p.window = window;
   p.sinks = sinks < T ? sinks : T;
   return cuda_status(launch_attn_prefill_window(mQ, mQs, mK, mV, p, d, S(stream)));
@@ -492,10 +494,12 @@ static gqe_status prefill_bwd_common(const gqe_dims* dims, const gqe_bf16* q_rou
   attn_bwd_layout(B, T, G, k, dims->n_shared, d, &L);
   const bool win = has_window(dims, window);
   const int n_sinks = sinks < T ? sinks : T;
-  AttnBwdWindowPlan P{};
-  P.bytes = L.bytes;
-  if (win) attn_bwd_window_plan(B, T, G, k, dims->n_shared, d, window, n_sinks, &P);
-  GQE_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && ws_bytes >= P.bytes, GQE_ERR_WORKSPACE);
+  AttnBwdSchedule sched;
+  size_t off_part = 0, need = L.bytes;
+  if (win)
+    attn_bwd_window_plan(B, T, G, k, dims->n_shared, dims->shared_kv_group, d, window, n_sinks, &sched, &off_part,
+                         &need);
+  GQE_REQUIRE(ws && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0 && ws_bytes >= need, GQE_ERR_WORKSPACE);
   uint8_t* w = static_cast<uint8_t*>(ws);
   CUtensorMap mQ, mQs, mdO, mdOs, mK, mV, mdQ;
   GQE_REQUIRE(map3d(&mQ, q_routed, d, (uint64_t)T * k, (uint64_t)B * G, 128), GQE_ERR_CUDA);
@@ -544,11 +548,8 @@ static gqe_status prefill_bwd_common(const gqe_dims* dims, const gqe_bf16* q_rou
   // weight is 1 whatever its score, so dS is 0 (and not the rounding that
   // dP - Delta would leave)
   if (window == 1 && n_sinks == 0) p.scale = 0.f;
-  p.sink_tiles = P.sink_tiles;
-  p.split_len = P.split_len;
-  p.n_parts = P.n_parts;
-  p.part = reinterpret_cast<float*>(w + P.off_part);
-  return cuda_status(launch_attn_bwd_window(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S(stream)));
+  p.part = reinterpret_cast<float*>(w + off_part);
+  return cuda_status(launch_attn_bwd_window(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, sched, S(stream)));
 }
 
 gqe_status gqe_attn_prefill_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
@@ -593,7 +594,7 @@ static gqe_status cache_attn_common(const gqe_dims* dims, const gqe_bf16* q_rout
   (void)ws;            // the shares are joined on chip: no scratch (gqe_window_workspace_size says 0)
   (void)ws_bytes;
   GQE_REQUIRE(P.items <= 0x7FFFFFFFll, GQE_ERR_UNSUPPORTED);
-  const uint32_t box = cache_attn_key_tile(d);
+  const uint32_t box = attn_window_key_tile(d);
   CUtensorMap mK, mV, mKt, mVt;
   GQE_REQUIRE(map3d(&mK, Kc, d, L_max, (uint64_t)B * G, box), GQE_ERR_CUDA);
   GQE_REQUIRE(map3d(&mV, Vc, d, L_max, (uint64_t)B * G, box), GQE_ERR_CUDA);
@@ -677,9 +678,10 @@ gqe_status gqe_window_workspace_size(const gqe_dims* dims, int op, int L_max, in
   const int B = dims->B, T = dims->T, G = dims->G, k = dims->k, d = dims->d_head;
   if (op == GQE_OP_ATTN_WINDOW_BWD) {
     if (!has_window(dims, window)) return gqe_workspace_size(dims, GQE_OP_ATTN_BWD, 0, bytes);
-    AttnBwdWindowPlan P;
-    attn_bwd_window_plan(B, T, G, k, dims->n_shared, d, window, sinks < T ? sinks : T, &P);
-    *bytes = P.bytes;
+    AttnBwdSchedule sched;
+    size_t off_part;
+    attn_bwd_window_plan(B, T, G, k, dims->n_shared, dims->shared_kv_group, d, window, sinks < T ? sinks : T, &sched,
+                         &off_part, bytes);
     return GQE_OK;
   }
   if (op == GQE_OP_ATTN_DECODE_WINDOW || op == GQE_OP_ATTN_TREE) {

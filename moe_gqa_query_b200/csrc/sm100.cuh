@@ -41,6 +41,12 @@ __device__ __forceinline__ unsigned long long globaltimer() {
 }
 
 __device__ __forceinline__ bool elect_lane0() { return (threadIdx.x & 31) == 0; }
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 // ---------------------------------------------------------------- dependent launch
 // Wait until the kernels this one depends on (the previous kernel on the
@@ -50,6 +56,19 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // Let the next kernel on the stream begin launching (its CTAs then wait in
 // pdl_wait before touching this kernel's data).
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" :::); }
+
+// ---------------------------------------------------------------- register split
+// Registers per thread of the calling warpgroup (four aligned warps, all of
+// them).  The shares of a CTA's warpgroups may not add up to more than its
+// threads times the registers it was launched with: set_regs_up waits for them.
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -114,6 +133,34 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       }
     }
   }
+}
+
+// The same bound in a few instructions: tries instead of the timer (each try
+// sleeps up to a microsecond, so the limit is between a tenth of a second and
+// two), and the code is recorded once, at the kernel's end (report_abort).
+// mbar_wait's slow path, inlined at every wait, was half of the windowed
+// backward's 66 KB, and its warps waited for instructions most of the time.
+constexpr uint32_t kWaitTries = 1u << 21;
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (uint32_t n = 0; n < kWaitTries; ++n) {
+    if (mbar_try_wait_sleep(bar, parity, 1000u)) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+// For a whole warp, with one answer.  A role that issues MMAs or TMA copies runs
+// its loop on all 32 lanes and only the instructions themselves on an elected
+// one: the compiler then keeps descriptors and addresses in uniform registers.
+// A role on one lane from the start moves every operand there first, about 25
+// instructions for each MMA.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_short(bar, parity, abort));
+}
+__device__ __forceinline__ void report_abort(volatile int* abort, unsigned* err, unsigned code) {
+  if (threadIdx.x == 0 && *abort && err) atomicCAS(err, 0u, code);
 }
 
 // After an abort, give copies already in flight time to land before the CTA
@@ -347,6 +394,9 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
+// The descriptor of the operand `bytes` further on.
+__device__ __forceinline__ uint64_t sdesc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
+
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                         uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -501,6 +551,12 @@ __device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsig
 __device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsigned long long b) {
   unsigned long long d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 
