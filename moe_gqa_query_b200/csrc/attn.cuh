@@ -86,7 +86,6 @@ struct AttnBwdLayout {
 };
 
 cudaError_t launch_attn_bwd_prep(const AttnBwdParams& p, cudaStream_t stream);
-cudaError_t launch_attn_bwd_post(const AttnBwdParams& p, cudaStream_t stream);
 
 // Windowed backward (attn_bwd_window.cu): where each CTA starts in the list of
 // (sequence, key tile, query tile of its walk), cut into equal stretches.

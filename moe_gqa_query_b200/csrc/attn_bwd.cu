@@ -609,11 +609,7 @@ __global__ void __launch_bounds__(256) attn_bwd_post_kernel(AttnBwdParams p) {
     dst = p.dq_sh + ((long long)b * p.T + r) * p.d;
   }
   const float4* a = reinterpret_cast<const float4*>(p.dq_acc + pr * p.d + part * 8);
-  float4 x = a[0], y = a[1];
-  if (p.window) {      // the windowed kernel leaves the scale of dS to this place
-    x.x *= p.scale, x.y *= p.scale, x.z *= p.scale, x.w *= p.scale;
-    y.x *= p.scale, y.y *= p.scale, y.z *= p.scale, y.w *= p.scale;
-  }
+  const float4 x = a[0], y = a[1];
   reinterpret_cast<uint4*>(dst)[part] =
       make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
 }
@@ -639,15 +635,12 @@ cudaError_t launch_attn_bwd_prep(const AttnBwdParams& p, cudaStream_t stream) {
   return launch_kernel(attn_bwd_prep_kernel, dim3((int)((threads + 255) / 256)), dim3(256), 0, stream, 1, p);
 }
 
-cudaError_t launch_attn_bwd_post(const AttnBwdParams& p, cudaStream_t stream) {
-  const long long threads = p.n_rows_pad * (p.d / 8);
-  return launch_kernel(attn_bwd_post_kernel, dim3((int)((threads + 255) / 256)), dim3(256), 0, stream, 1, p);
-}
-
 cudaError_t launch_attn_bwd(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
                             const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
                             const CUtensorMap& mdQ, const AttnBwdParams& p, cudaStream_t stream) {
   if (p.d != 64 && p.d != 128) return cudaErrorNotSupported;
+  const long long threads = p.n_rows_pad * (p.d / 8);
+  const int blocks = (int)((threads + 255) / 256);
   cudaError_t e = launch_attn_bwd_prep(p, stream);
   if (e != cudaSuccess) return e;
   auto kern = p.d == 64 ? attn_bwd_kernel<64> : attn_bwd_kernel<128>;
@@ -658,7 +651,7 @@ cudaError_t launch_attn_bwd(const CUtensorMap& mQ, const CUtensorMap& mQs, const
   e = launch_kernel(kern, dim3(n_kvt * p.B * p.G), dim3(kBwdThreads), smem, stream, 1, mQ, mQs, mdO, mdOs, mK, mV,
                     mdQ, p);
   if (e != cudaSuccess) return e;
-  return launch_attn_bwd_post(p, stream);
+  return launch_kernel(attn_bwd_post_kernel, dim3(blocks), dim3(256), 0, stream, 1, p);
 }
 
 }  // namespace gqe

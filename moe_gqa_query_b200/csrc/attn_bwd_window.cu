@@ -16,7 +16,7 @@
 // CTA runs its stretch as one pipeline: the loads and products of the next key
 // tile start while the last one's are still running.  A walk cut by a stretch's
 // end leaves its dK, dV sums in fp32 in a slot of its CTA, and
-// attn_bwd_window_join_kernel adds the slots of a walk in their order, so dK
+// attn_bwd_window_post_kernel adds the slots of a walk in their order, so dK
 // and dV do not depend on timing.  dQ goes through TMA reduce-add into fp32 as
 // in attn_bwd.cu.
 //
@@ -548,43 +548,43 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
       // d = 128 the next dP^T waits for the dQ drain, so that comes first.
 #pragma unroll 1
       for (int step = 0; step < 2; ++step) {
-      if ((step == 0) != C::kWide) {
-        if (!c.last()) continue;
-        if (!wait(&bar->pv_done, N) || !wait(&bar->dk_done, N)) goto out;
+        if ((step == 0) != C::kWide) {
+          if (!c.last()) continue;
+          if (!wait(&bar->pv_done, N) || !wait(&bar->dk_done, N)) goto out;
+          tc_fence_after();
+          read_acc<D>(c, p, tmem + lane_off, qd * 32 + lane, &bar->acc_free);
+          continue;
+        }
+        if (!wait(&bar->dq_full, N)) goto out;
         tc_fence_after();
-        read_acc<D>(c, p, tmem + lane_off, qd * 32 + lane, &bar->acc_free);
-        continue;
-      }
-      if (!wait(&bar->dq_full, N)) goto out;
-      tc_fence_after();
-      const int row_pad = c.row_pad(p);
+        const int row_pad = c.row_pad(p);
 #pragma unroll
-      for (int g0 = 0; g0 < D / 32; g0 += C::EpiCh) {
-        // staging free: every earlier reduce of this warp has read it
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
+        for (int g0 = 0; g0 < D / 32; g0 += C::EpiCh) {
+          // staging free: every earlier reduce of this warp has read it
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < C::EpiCh; ++i) {
-          uint32_t v[32];
-          tmem_ld32(tmem + lane_off + C::kDQ + (g0 + i) * 32, v);
-          if (g0 + i == D / 32 - 1) {
-            tc_fence_before();
-            mbar_arrive(&bar->dq_free);
+          for (int i = 0; i < C::EpiCh; ++i) {
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_off + C::kDQ + (g0 + i) * 32, v);
+            if (g0 + i == D / 32 - 1) {
+              tc_fence_before();
+              mbar_arrive(&bar->dq_free);
+            }
+            uint8_t* rowp = stage + i * 4096 + lane * 128;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(rowp + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           }
-          uint8_t* rowp = stage + i * 4096 + lane * 128;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            st_shared_v4(rowp + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            for (int i = 0; i < C::EpiCh; ++i)
+              tma_reduce_add_2d(&mapdQ, stage + i * 4096, (g0 + i) * 32, row_pad + qd * 32);
+            bulk_commit();
+          }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-#pragma unroll
-          for (int i = 0; i < C::EpiCh; ++i)
-            tma_reduce_add_2d(&mapdQ, stage + i * 4096, (g0 + i) * 32, row_pad + qd * 32);
-          bulk_commit();
-        }
-      }
       }
       ++N;
     } while (c.next(p));
@@ -601,13 +601,11 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
   drain_after_abort(abort);
 }
 
-// dK, dV of the walks that the stretches' ends cut: block c adds the pieces of
-// the walk cut between CTAs c-1 and c, when that is the walk's first cut.
-__global__ void __launch_bounds__(256)
-attn_bwd_window_join_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnBwdSchedule S) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int c = blockIdx.x + 1;
+// dK, dV of a walk that the stretches' ends cut: the pieces of the walk cut
+// between CTAs c-1 and c added in their order, when that is the walk's first cut.
+// Each of the kJoinBlocks blocks takes its part of the tile.
+constexpr int kJoinBlocks = 8;
+__device__ __forceinline__ void join_walk(const AttnBwdParams& p, const AttnBwdSchedule& S, int c, int block) {
   const int s = S.seq[c], jt = S.jt[c];
   if (S.off[c] == 0) return;                                                     // the walk starts here
   if (S.seq[c - 1] == s && S.jt[c - 1] == jt && S.off[c - 1] > 0) return;         // cut before
@@ -615,7 +613,7 @@ attn_bwd_window_join_kernel(const __grid_constant__ AttnBwdParams p, const __gri
   while (last + 1 < S.n_ctas && S.seq[last + 1] == s && S.jt[last + 1] == jt && S.off[last + 1] > 0) ++last;
   const size_t slot = (size_t)2 * kTileW * p.d;
   const int per = p.d / 4;
-  for (int e = blockIdx.y * 256 + threadIdx.x; e < 2 * kTileW * per; e += gridDim.y * 256) {
+  for (int e = block * 256 + threadIdx.x; e < 2 * kTileW * per; e += kJoinBlocks * 256) {
     const int c4 = e % per, row = e / per % kTileW, which = e / per / kTileW;
     const int kv_pos = jt * kTileW + row;
     if (kv_pos >= p.T) continue;
@@ -629,6 +627,40 @@ attn_bwd_window_join_kernel(const __grid_constant__ AttnBwdParams p, const __gri
     gqe_bf16_t* dst = (which ? p.dV : p.dK) + ((size_t)s * p.T + kv_pos) * p.d;
     reinterpret_cast<uint2*>(dst)[c4] = make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
   }
+}
+
+// The first (n_ctas - 1) * kJoinBlocks blocks join the cut walks, the others
+// round dq from its fp32 sums (d/8 threads a row, valid rows only).
+__global__ void __launch_bounds__(256)
+attn_bwd_window_post_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnBwdSchedule S) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n_join = (S.n_ctas - 1) * kJoinBlocks;
+  if ((int)blockIdx.x < n_join) {
+    join_walk(p, S, blockIdx.x / kJoinBlocks + 1, blockIdx.x % kJoinBlocks);
+    return;
+  }
+  const int tpr = p.d / 8;
+  const long long gt = (long long)(blockIdx.x - n_join) * 256 + threadIdx.x;
+  const long long pr = gt / tpr, routed_rows = (long long)p.B * p.G * p.rows_pad;
+  const int part = (int)(gt % tpr);
+  if (pr >= p.n_rows_pad) return;
+  gqe_bf16_t* dst;
+  if (pr < routed_rows) {
+    const int sq = (int)(pr / p.rows_pad), r = (int)(pr % p.rows_pad);
+    if (r >= p.T * p.k) return;
+    dst = p.dq_routed + ((long long)sq * p.T * p.k + r) * p.d;
+  } else {
+    const long long q2 = pr - routed_rows;
+    const int b = (int)(q2 / p.rows_pad_sh), r = (int)(q2 % p.rows_pad_sh);
+    if (r >= p.T) return;
+    dst = p.dq_sh + ((long long)b * p.T + r) * p.d;
+  }
+  const float4* a = reinterpret_cast<const float4*>(p.dq_acc + pr * p.d + part * 8);
+  const float4 x = a[0], y = a[1];
+  const float f = p.scale;
+  reinterpret_cast<uint4*>(dst)[part] = make_uint4(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f),
+                                                   pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
 }
 
 }  // namespace
@@ -701,11 +733,8 @@ cudaError_t launch_attn_bwd_window(const CUtensorMap& mQ, const CUtensorMap& mQs
   e = p.d == 64 ? launch_win<64>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S, stream)
                 : launch_win<128>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S, stream);
   if (e != cudaSuccess) return e;
-  if (S.n_ctas > 1) {
-    e = launch_kernel(attn_bwd_window_join_kernel, dim3(S.n_ctas - 1, 8), dim3(256), 0, stream, 1, p, S);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_attn_bwd_post(p, stream);
+  const long long blocks = (p.n_rows_pad * (p.d / 8) + 255) / 256 + (S.n_ctas - 1) * kJoinBlocks;
+  return launch_kernel(attn_bwd_window_post_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, 1, p, S);
 }
 
 }  // namespace gqe

@@ -62,7 +62,7 @@ struct __align__(16) CacheShared {
   int up[2][kMaxTree];               // pointer doubling: 2^r levels up, -1 past the root
   int depth[2][kMaxTree];
   float m[kRowsQ], l[kRowsQ];        // per lane
-  float row_m[kRowsQ], row_l[kRowsQ];   // per row, its repeats joined
+  float2 row_ml[kRowsQ];             // per row, its repeats joined
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
   uint64_t s_full, s_free, p_full, pv_done;
   uint32_t tmem_base;
@@ -196,17 +196,24 @@ __device__ __forceinline__ RowState cache_softmax(const CacheAttnParams& p, cons
       }
     }
     const float neg_m = st.m == -INFINITY ? 0.f : -st.m;     // nothing seen yet: every exponential is 0
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const unsigned long long sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(neg_m, neg_m);
+    unsigned long long sum2[2] = {0ull, 0ull};
     uint32_t pk[NC / 2];
 #pragma unroll
     for (int c = 0; c < NC / 2; ++c) {
-      const float p0 = ex2(fmaf(__uint_as_float(s[2 * c]), sl2, neg_m));
-      const float p1 = ex2(fmaf(__uint_as_float(s[2 * c + 1]), sl2, neg_m));
-      sum[(c & 1) * 2] += p0;
-      sum[(c & 1) * 2 + 1] += p1;
-      pk[c] = pack_bf16x2(p0, p1);
+      float x0, x1;
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2x2, negm2), x0, x1);
+      x0 = ex2(x0);
+      x1 = ex2(x1);
+      sum2[c & 1] = f2_add(sum2[c & 1], f2_pack(x0, x1));
+      pk[c] = pack_bf16x2(x0, x1);
     }
-    st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    {
+      float a0, a1, b0, b1;
+      f2_unpack(sum2[0], a0, a1);
+      f2_unpack(sum2[1], b0, b1);
+      st.l += (a0 + a1) + (b0 + b1);
+    }
     if (j > 0) {
       // P(j-1) V must be done before P is overwritten and O rescaled
       st.ok = mbar_wait_short(&sh->pv_done, (j - 1) & 1, abort) && st.ok;
@@ -231,10 +238,8 @@ __device__ __forceinline__ RowState cache_softmax(const CacheAttnParams& p, cons
       const int r = threadIdx.x, pos = kb + r;
       if (r < KT && (in_tree ? pos >= cl.m : pos >= cl.len || (pos < cl.lo0 && pos >= p.sinks))) {
         uint8_t* row = sV + (j % C::VST) * C::KVBytes + r * 128;
-#pragma unroll
-        for (int bx = 0; bx < C::NB; ++bx)
-#pragma unroll
-          for (int q = 0; q < 8; ++q) st_shared_v4(row + bx * C::KBox + q * 16, 0u, 0u, 0u, 0u);
+#pragma unroll 1
+        for (int q = 0; q < C::NB * 8; ++q) st_shared_v4(row + (q >> 3) * C::KBox + (q & 7) * 16, 0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
     }
@@ -247,14 +252,22 @@ __device__ __forceinline__ RowState cache_softmax(const CacheAttnParams& p, cons
   return st;
 }
 
-// Where packed row r of group (b, g) lives: token-major, the k routed rows,
-// then the shared head's when the group carries it (kr = k + 1).
-template <typename T>
-__device__ __forceinline__ T* row_ptr(T* routed, T* shared, const CacheAttnParams& p, int bg, int r, int kr, int D) {
-  const int t = r / kr, j = r % kr;
-  return j < p.k ? routed + ((size_t)((size_t)bg * p.T + t) * p.k + j) * D
-                 : shared + ((size_t)(bg / p.G) * p.T + t) * D;
-}
+// The packed rows of group (b, g): token-major, the k routed rows, then the
+// shared head's when the group carries it (kr = k + 1).
+struct RowMap {
+  int k, kr;
+  unsigned inv;        // ceil(2^20 / kr): r / kr is exact for r < 1152 and kr <= 9
+  size_t routed, shared;    // first element of the group's routed rows, of the sequence's shared rows
+  __device__ __forceinline__ RowMap(const CacheAttnParams& p, int bg, int b, int kr_, int D)
+      : k(p.k), kr(kr_), inv(((1u << 20) + kr_ - 1) / kr_), routed((size_t)bg * p.T * p.k * D),
+        shared((size_t)b * p.T * D) {}
+  __device__ __forceinline__ int token(int r) const { return (int)((r * inv) >> 20); }
+  template <typename T>
+  __device__ __forceinline__ T* at(T* q_routed, T* q_sh, int r, int D) const {
+    const int t = token(r), j = r - t * kr;
+    return j < k ? q_routed + routed + (size_t)(t * k + j) * D : q_sh + shared + (size_t)t * D;
+  }
+};
 
 // Ancestor bits and depths of the drafted tokens by pointer doubling, on the
 // 128 threads of the softmax warps: after round r a token's bits cover
@@ -309,8 +322,8 @@ __device__ __forceinline__ int build_tree(const CacheAttnParams& p, const CacheL
 // nothing get 0.  Every thread of the CTA calls it; a CTA leaves only when the
 // others have read its shared memory.
 template <int D>
-__device__ __forceinline__ void join_shares(const CacheAttnParams& p, CacheShared* sh, const uint8_t* smem, int bg,
-                                            int row0, int n_rows, int kr) {
+__device__ __forceinline__ void join_shares(const CacheAttnParams& p, CacheShared* sh, const uint8_t* smem,
+                                            const RowMap& rows, int row0, int n_rows) {
   constexpr int OPitch = CacheCfg<D>::OPitch;
   const float* sO = reinterpret_cast<const float*>(smem);
   const int share = blockIdx.x % p.n_split;
@@ -320,66 +333,50 @@ __device__ __forceinline__ void join_shares(const CacheAttnParams& p, CacheShare
   }
   const bool ok = *static_cast<volatile int*>(&sh->abort) == 0;
   // S lanes (a power of two) take one four-column piece of a row, each S-th
-  // share, and U pieces at once (remote reads take about 0.6 us: with one piece
-  // in flight per lane, 128 rows of d = 128 in 3 shares took 8 us)
-  constexpr int U = 4;
+  // share.  One piece at a time: with two or four in flight per lane 128 rows in
+  // three shares took 3 % less, but a few rows 4 and 9 % more, for the code.
   int S = 1;
   while (S * 2 <= p.n_split) S *= 2;
   const int n_units = n_rows * (D / 4), per_cta = kCacheThreads / S;
   const int sub = threadIdx.x % S;
-  for (int u0 = share * per_cta + threadIdx.x / S; __any_sync(0xffffffffu, u0 < n_units);
-       u0 += U * p.n_split * per_cta) {
-    float m[U][2], l[U][2];
-    float4 x[U][2];
+  for (int u = share * per_cta + threadIdx.x / S; __any_sync(0xffffffffu, u < n_units); u += p.n_split * per_cta) {
+    const int er = u / (D / 4), c4 = u % (D / 4);
+    float2 ml[2];
+    float4 x[2];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int u = u0 + i * p.n_split * per_cta, er = u / (D / 4), c4 = u % (D / 4);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {      // n_split < 2 S: at most two shares per lane
-        const int c = sub + h * S;
-        m[i][h] = -INFINITY;
-        l[i][h] = 0.f;
-        x[i][h] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ok && u < n_units && c < p.n_split) {
-          if (p.n_split == 1) {
-            m[i][h] = sh->row_m[er];
-            l[i][h] = sh->row_l[er];
-            x[i][h] = reinterpret_cast<const float4*>(sO + er * OPitch)[c4];
-          } else {
-            m[i][h] = ld_cluster_f32(cluster_map(smem_u32(&sh->row_m[er]), c));
-            l[i][h] = ld_cluster_f32(cluster_map(smem_u32(&sh->row_l[er]), c));
-            x[i][h] = ld_cluster_f32x4(cluster_map(smem_u32(sO + er * OPitch + c4 * 4), c));
-          }
-        }
+    for (int h = 0; h < 2; ++h) {        // n_split < 2 S: at most two shares per lane
+      const int c = sub + h * S;
+      ml[h] = make_float2(-INFINITY, 0.f);
+      x[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ok && u < n_units && c < p.n_split) {
+        // (one CTA reads itself through the same instructions: rank 0 of 1)
+        ml[h] = ld_cluster_f32x2(cluster_map(smem_u32(&sh->row_ml[er]), c));
+        x[h] = ld_cluster_f32x4(cluster_map(smem_u32(sO + er * OPitch + c4 * 4), c));
       }
     }
+    float M = fmaxf(ml[0].x, ml[1].x), Ls = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int o = 1; o < S; o *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int u = u0 + i * p.n_split * per_cta, er = u / (D / 4), c4 = u % (D / 4);
-      float M = fmaxf(m[i][0], m[i][1]), Ls = 0.f;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int o = 1; o < S; o *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (m[i][h] > -INFINITY) {       // else the share saw nothing and its O was not written
-          const float f = ex2(m[i][h] - M);
-          Ls = fmaf(l[i][h], f, Ls);
-          a.x = fmaf(x[i][h].x, f, a.x), a.y = fmaf(x[i][h].y, f, a.y);
-          a.z = fmaf(x[i][h].z, f, a.z), a.w = fmaf(x[i][h].w, f, a.w);
-        }
+    for (int h = 0; h < 2; ++h) {
+      if (ml[h].y != 0.f) {              // else the share saw nothing and its O was not written
+        const float f = ex2(ml[h].x - M);
+        Ls = fmaf(ml[h].y, f, Ls);
+        a.x = fmaf(x[h].x, f, a.x), a.y = fmaf(x[h].y, f, a.y);
+        a.z = fmaf(x[h].z, f, a.z), a.w = fmaf(x[h].w, f, a.w);
       }
-      for (int o = 1; o < S; o *= 2) {
-        Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
-        a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
-        a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
-        a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
-        a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
-      }
-      const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
-      if (ok && u < n_units && sub == 0)
-        reinterpret_cast<uint2*>(row_ptr(p.o_routed, p.o_sh, p, bg, row0 + er, kr, D))[c4] =
-            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     }
+    for (int o = 1; o < S; o *= 2) {
+      Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+      a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+      a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+      a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+      a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+    }
+    const float inv = Ls == 0.f ? 0.f : 1.f / Ls;        // a NaN sum stays one
+    if (ok && u < n_units && sub == 0)
+      reinterpret_cast<uint2*>(rows.at(p.o_routed, p.o_sh, row0 + er, D))[c4] =
+          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
   }
   if (p.n_split > 1) {
     __syncwarp();
@@ -423,193 +420,186 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
       atomicCAS(p.err, 0u, (unsigned)kErrTreeArgs);
   }
   const CacheList cl = cache_list<KT>(p, b);
+  const RowMap rows(p, bg, b, kr, D);
   const int first = (int)((long long)cl.n * share / p.n_split);
-  const int n = row0 / kr < cl.m ? (int)((long long)cl.n * (share + 1) / p.n_split) - first : 0;
+  const int n = rows.token(row0) < cl.m ? (int)((long long)cl.n * (share + 1) / p.n_split) - first : 0;
 
   if (n == 0) {
     // an empty share: its rows saw nothing
-    for (int e = tid; e < n_rows; e += kCacheThreads) {
-      sh->row_m[e] = -INFINITY;
-      sh->row_l[e] = 0.f;
-    }
+    if (tid < n_rows) sh->row_ml[tid] = make_float2(-INFINITY, 0.f);
     if (tid == 0) sh->abort = 0;
     __syncthreads();
-    join_shares<D>(p, sh, smem, bg, row0, n_rows, kr);
-    return;
-  }
-
-  auto load_k = [&](int j) {
-    const int s = j % KST, i = first + j;
-    const CUtensorMap* map = i < cl.n_cache ? &mapK : &mapKt;
-    mbar_arrive_expect_tx(&sh->k_full[s], C::KVBytes);
-    for (int bx = 0; bx < C::NB; ++bx)
-      tma_load_3d(sK + s * C::KVBytes + bx * C::KBox, map, &sh->k_full[s], bx * 64, cl.row<KT>(i), bg);
-  };
-  auto load_v = [&](int j) {
-    const int s = j % VST, i = first + j;
-    const CUtensorMap* map = i < cl.n_cache ? &mapV : &mapVt;
-    mbar_arrive_expect_tx(&sh->v_full[s], C::KVBytes);
-    for (int bx = 0; bx < C::NB; ++bx)
-      tma_load_3d(sV + s * C::KVBytes + bx * C::KBox, map, &sh->v_full[s], bx * 64, cl.row<KT>(i), bg);
-  };
-  if (warp == 4 && lane == 0) {
-    for (int s = 0; s < KST; ++s) {
-      mbar_init(&sh->k_full[s], 1);
-      mbar_init(&sh->k_empty[s], 1);
-    }
-    for (int s = 0; s < VST; ++s) {
-      mbar_init(&sh->v_full[s], 1);
-      mbar_init(&sh->v_empty[s], 1);
-    }
-    mbar_init(&sh->s_full, 1);
-    mbar_init(&sh->s_free, 128);
-    mbar_init(&sh->p_full, 128);
-    mbar_init(&sh->pv_done, 1);
-    sh->abort = 0;
-    fence_mbar_init();
-    for (int j = 0; j < KST && j < n; ++j) {
-      load_k(j);
-      if (j < VST) load_v(j);
-    }
-  }
-  if (warp == 5) tmem_alloc(&sh->tmem_base, 256);
-  const int up = p.tree && tid < cl.m ? p.parent[(size_t)b * p.T + tid] : -1;
-  // Q rows, repeated `rep` times, into the 128-byte swizzled layout (every load
-  // in flight before the first store: one trip to memory)
-  {
-    constexpr int NL = (kRowsQ * (D / 8) + kCacheThreads - 1) / kCacheThreads;
-    uint4 v[NL];
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int e = tid + i * kCacheThreads, r = e / (D / 8);
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (r < n_rows) v[i] = reinterpret_cast<const uint4*>(row_ptr(p.q_routed, p.q_sh, p, bg, row0 + r, kr, D))[e % (D / 8)];
-    }
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int e = tid + i * kCacheThreads, c = e % (D / 8);
-      if (e / (D / 8) < lanes_rep)
-        for (int L = e / (D / 8); L < kRowsQ; L += lanes_rep)
-          st_shared_v4(sQ + (c >> 3) * C::QBox + L * 128 + (((c & 7) ^ (L & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
-    }
-  }
-  fence_proxy_async_smem();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh->tmem_base;
-
-  if (warp == 4) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kRowsQ, KT, false, false);
-      const uint32_t q0 = smem_u32(sQ);
-      bool ok = true;
-      for (int j = 0; ok && j < n; ++j) {
-        const int s = j % KST;
-        if (j > 0) ok = mbar_wait_short(&sh->s_free, (j - 1) & 1, abort);
-        ok = ok && mbar_wait_short(&sh->k_full[s], (j / KST) & 1, abort);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t k0 = smem_u32(sK + s * C::KVBytes);
-        const uint64_t dq = sdesc_sw128(q0, 16, 1024), dk = sdesc_sw128(k0, 16, 1024);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_ss(tmem + C::kS, sdesc_at(dq, (ks >> 2) * C::QBox + (ks & 3) * 32),
-                  sdesc_at(dk, (ks >> 2) * C::KBox + (ks & 3) * 32), idesc_s, ks > 0);
-        umma_commit(&sh->s_full);
-        umma_commit(&sh->k_empty[s]);
-        if (j + KST < n) {
-          ok = mbar_wait_short(&sh->k_empty[s], (j / KST) & 1, abort);
-          if (!ok) break;
-          load_k(j + KST);
-        }
+  } else {
+    auto load_k = [&](int j) {
+      const int s = j % KST, i = first + j;
+      const CUtensorMap* map = i < cl.n_cache ? &mapK : &mapKt;
+      mbar_arrive_expect_tx(&sh->k_full[s], C::KVBytes);
+      for (int bx = 0; bx < C::NB; ++bx)
+        tma_load_3d(sK + s * C::KVBytes + bx * C::KBox, map, &sh->k_full[s], bx * 64, cl.row<KT>(i), bg);
+    };
+    auto load_v = [&](int j) {
+      const int s = j % VST, i = first + j;
+      const CUtensorMap* map = i < cl.n_cache ? &mapV : &mapVt;
+      mbar_arrive_expect_tx(&sh->v_full[s], C::KVBytes);
+      for (int bx = 0; bx < C::NB; ++bx)
+        tma_load_3d(sV + s * C::KVBytes + bx * C::KBox, map, &sh->v_full[s], bx * 64, cl.row<KT>(i), bg);
+    };
+    if (warp == 4 && lane == 0) {
+      for (int s = 0; s < KST; ++s) {
+        mbar_init(&sh->k_full[s], 1);
+        mbar_init(&sh->k_empty[s], 1);
+      }
+      for (int s = 0; s < VST; ++s) {
+        mbar_init(&sh->v_full[s], 1);
+        mbar_init(&sh->v_empty[s], 1);
+      }
+      mbar_init(&sh->s_full, 1);
+      mbar_init(&sh->s_free, 128);
+      mbar_init(&sh->p_full, 128);
+      mbar_init(&sh->pv_done, 1);
+      sh->abort = 0;
+      fence_mbar_init();
+      for (int j = 0; j < KST && j < n; ++j) {
+        load_k(j);
+        if (j < VST) load_v(j);
       }
     }
-  } else if (warp == 5) {
-    if (lane == 0) {
+    if (warp == 5) tmem_alloc(&sh->tmem_base, 256);
+    const int up = p.tree && tid < cl.m ? p.parent[(size_t)b * p.T + tid] : -1;
+    // Q rows, repeated `rep` times, into the 128-byte swizzled layout (every load
+    // in flight before the first store: one trip to memory)
+    {
+      constexpr int NL = (kRowsQ * (D / 8) + kCacheThreads - 1) / kCacheThreads;
+      uint4 v[NL];
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int e = tid + i * kCacheThreads, r = e / (D / 8);
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r < n_rows) v[i] = reinterpret_cast<const uint4*>(rows.at(p.q_routed, p.q_sh, row0 + r, D))[e % (D / 8)];
+      }
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int e = tid + i * kCacheThreads, c = e % (D / 8);
+        if (e / (D / 8) < lanes_rep)
+          for (int L = e / (D / 8); L < kRowsQ; L += lanes_rep)
+            st_shared_v4(sQ + (c >> 3) * C::QBox + L * 128 + (((c & 7) ^ (L & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_base;
+
+    if (warp == 4) {
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kRowsQ, KT, false, false);
+      const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      for (int j = 0; j < n; ++j) {
+        const int s = j % KST;
+        if (j > 0 && !mbar_wait_warp(&sh->s_free, (j - 1) & 1, abort)) break;
+        if (!mbar_wait_warp(&sh->k_full[s], (j / KST) & 1, abort)) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t dk = sdesc_sw128(smem_u32(sK + s * C::KVBytes), 16, 1024);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_ss(tmem + C::kS, sdesc_at(dq, (ks >> 2) * C::QBox + (ks & 3) * 32),
+                    sdesc_at(dk, (ks >> 2) * C::KBox + (ks & 3) * 32), idesc_s, ks > 0);
+          umma_commit(&sh->s_full);
+          umma_commit(&sh->k_empty[s]);
+        }
+        if (j + KST < n) {
+          if (!mbar_wait_warp(&sh->k_empty[s], (j / KST) & 1, abort)) break;
+          if (leader) load_k(j + KST);
+        }
+      }
+    } else if (warp == 5) {
+      const bool leader = elect_one();
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRowsQ, D, false, true);
       for (int j = 0; j < n; ++j) {
         const int s = j % VST;
-        if (!mbar_wait_short(&sh->p_full, j & 1, abort)) break;
-        if (!mbar_wait_short(&sh->v_full[s], (j / VST) & 1, abort)) break;
+        if (!mbar_wait_warp(&sh->p_full, j & 1, abort)) break;
+        if (!mbar_wait_warp(&sh->v_full[s], (j / VST) & 1, abort)) break;
         tc_fence_after();
-        const uint32_t v0 = smem_u32(sV + s * C::KVBytes);
-        const uint64_t dv = sdesc_sw128(v0, C::KBox, 1024);
+        if (leader) {
+          const uint64_t dv = sdesc_sw128(smem_u32(sV + s * C::KVBytes), C::KBox, 1024);
 #pragma unroll
-        for (int ks = 0; ks < KT / 16; ++ks)
-          umma_ts(tmem + C::kO, tmem + C::kP + ks * 8, sdesc_at(dv, ks * 2048), idesc_o, (j > 0 || ks > 0));
-        umma_commit(&sh->pv_done);
-        umma_commit(&sh->v_empty[s]);
+          for (int ks = 0; ks < KT / 16; ++ks)
+            umma_ts(tmem + C::kO, tmem + C::kP + ks * 8, sdesc_at(dv, ks * 2048), idesc_o, (j > 0 || ks > 0));
+          umma_commit(&sh->pv_done);
+          umma_commit(&sh->v_empty[s]);
+        }
         if (j + VST < n) {
-          if (!mbar_wait_short(&sh->v_empty[s], (j / VST) & 1, abort)) break;
-          load_v(j + VST);
+          if (!mbar_wait_warp(&sh->v_empty[s], (j / VST) & 1, abort)) break;
+          if (leader) load_v(j + VST);
         }
       }
-    }
-  } else {
-    // ---------------- softmax: warps 0-3, one lane per (row, repeat)
-    const int cur = p.tree ? build_tree(p, cl, sh, up) : 0;
-    const int r = tid % lanes_rep, q = tid / lanes_rep;
-    const int t_r = (row0 + r) / kr;
-    const bool live = r < n_rows && t_r < cl.m;
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    const int depth = p.tree && live ? sh->depth[cur][t_r] : 0;
-    const uint32_t* anc = reinterpret_cast<const uint32_t*>(&sh->anc[cur][live ? t_r : 0]);
-    RowState st;
-    if (rep == 4)
-      st = cache_softmax<D, KT / 4>(p, cl, sh, sV, lane_base, first, n, q * (KT / 4), t_r, anc, depth);
-    else if (rep == 2)
-      st = cache_softmax<D, KT / 2>(p, cl, sh, sV, lane_base, first, n, q * (KT / 2), t_r, anc, depth);
-    else
-      st = cache_softmax<D, KT>(p, cl, sh, sV, lane_base, first, n, 0, t_r, anc, depth);
-    // ---------------- epilogue: join the repeats through shared memory (the
-    // operand tiles are no longer read)
-    float* sO = reinterpret_cast<float*>(smem);
-    sh->m[tid] = live ? st.m : -INFINITY;
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    float M = -INFINITY;
-    for (int i = 0; i < rep; ++i) M = fmaxf(M, sh->m[r + i * lanes_rep]);
-    const float f = live && st.m > -INFINITY ? ex2(st.m - M) : 0.f;
-    sh->l[tid] = f > 0.f ? st.l * f : 0.f;
+    } else {
+      // ---------------- softmax: warps 0-3, one lane per (row, repeat)
+      const int cur = p.tree ? build_tree(p, cl, sh, up) : 0;
+      const int r = tid % lanes_rep, q = tid / lanes_rep;
+      const int t_r = rows.token(row0 + r);
+      const bool live = r < n_rows && t_r < cl.m;
+      const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+      const int depth = p.tree && live ? sh->depth[cur][t_r] : 0;
+      const uint32_t* anc = reinterpret_cast<const uint32_t*>(&sh->anc[cur][live ? t_r : 0]);
+      RowState st;
+      if (rep == 4)
+        st = cache_softmax<D, KT / 4>(p, cl, sh, sV, lane_base, first, n, q * (KT / 4), t_r, anc, depth);
+      else if (rep == 2)
+        st = cache_softmax<D, KT / 2>(p, cl, sh, sV, lane_base, first, n, q * (KT / 2), t_r, anc, depth);
+      else
+        st = cache_softmax<D, KT>(p, cl, sh, sV, lane_base, first, n, 0, t_r, anc, depth);
+      // ---------------- epilogue: join the repeats through shared memory (the
+      // operand tiles are no longer read)
+      float* sO = reinterpret_cast<float*>(smem);
+      sh->m[tid] = live ? st.m : -INFINITY;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      float M = -INFINITY;
+      for (int i = 0; i < rep; ++i) M = fmaxf(M, sh->m[r + i * lanes_rep]);
+      const bool saw = live && st.l != 0.f;       // (a NaN sum is one too, and reaches the output)
+      const float f = saw ? ex2(st.m - M) : 0.f;
+      sh->l[tid] = saw ? st.l * f : 0.f;
 #pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += 32) {
-      uint32_t o[32];
-      tmem_ld32(lane_base + C::kO + c0, o);
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
+        tmem_ld32(lane_base + C::kO + c0, o);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (f > 0.f)
-          v = make_float4(__uint_as_float(o[4 * c]) * f, __uint_as_float(o[4 * c + 1]) * f,
-                          __uint_as_float(o[4 * c + 2]) * f, __uint_as_float(o[4 * c + 3]) * f);
-        reinterpret_cast<float4*>(sO + tid * C::OPitch + c0)[c] = v;
+        for (int c = 0; c < 8; ++c) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (saw)
+            v = make_float4(__uint_as_float(o[4 * c]) * f, __uint_as_float(o[4 * c + 1]) * f,
+                            __uint_as_float(o[4 * c + 2]) * f, __uint_as_float(o[4 * c + 3]) * f);
+          reinterpret_cast<float4*>(sO + tid * C::OPitch + c0)[c] = v;
+        }
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      // the sum over a row's repeats replaces its first repeat
+      for (int e = tid; rep > 1 && e < n_rows * (D / 4); e += 128) {
+        const int er = e / (D / 4), c4 = e % (D / 4);
+        float4* first_o = reinterpret_cast<float4*>(sO + er * C::OPitch) + c4;
+        float4 a = *first_o;
+        for (int i = 1; i < rep; ++i) {
+          const float4 x = reinterpret_cast<const float4*>(sO + (er + i * lanes_rep) * C::OPitch)[c4];
+          a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+        }
+        *first_o = a;
+      }
+      if (tid < n_rows) {
+        float Ls = 0.f;
+        for (int i = 0; i < rep; ++i) Ls += sh->l[tid + i * lanes_rep];
+        sh->row_ml[tid] = make_float2(M, Ls);
       }
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    // the sum over a row's repeats replaces its first repeat
-    for (int e = tid; rep > 1 && e < n_rows * (D / 4); e += 128) {
-      const int er = e / (D / 4), c4 = e % (D / 4);
-      float4* first_o = reinterpret_cast<float4*>(sO + er * C::OPitch) + c4;
-      float4 a = *first_o;
-      for (int i = 1; i < rep; ++i) {
-        const float4 x = reinterpret_cast<const float4*>(sO + (er + i * lanes_rep) * C::OPitch)[c4];
-        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-      }
-      *first_o = a;
-    }
-    if (tid < n_rows) {
-      float Ls = 0.f;
-      for (int i = 0; i < rep; ++i) Ls += sh->l[tid + i * lanes_rep];
-      sh->row_m[tid] = M;
-      sh->row_l[tid] = Ls;
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+      tc_fence_after();
+      tmem_dealloc(tmem, 256);
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 5) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 256);
-  }
-  join_shares<D>(p, sh, smem, bg, row0, n_rows, kr);
+  join_shares<D>(p, sh, smem, rows, row0, n_rows);
   report_abort(abort, p.err, kErrTimeoutCacheAttn);
   drain_after_abort(abort);
 }

@@ -281,6 +281,21 @@ def test_tree_sharp_scores():
     close(os_, rs, bs, "o_sh")
 
 
+def test_tree_a_nan_query_stays_in_its_row():
+    """A NaN in one live token's query makes that row NaN and leaves the others alone."""
+    for shape in (D(T=6, B=2), D(T=100, B=1, n_shared=0), D(T=5, B=1, d=128)):
+        L, B = 700, shape.B
+        x = _cache_inputs(shape, L, 20)
+        parent = random_parents(B, shape.T, 20)
+        (ro, _), (bo, _) = ow.attn_tree(x["q"], x["qs"], x["K"], x["V"], parent, [shape.T] * B, x["Kc"], x["Vc"], [600] * B,
+                                        shape, 0, 0)
+        x["q"][0, 1, 3, 0, 7] = 0x7FC0
+        _, o, _ = _run_tree(shape, L, [600] * B, None, parent, x, 0, 0, poison=False)
+        assert torch.isnan(o[0, 1, 3]).all()
+        o[0, 1, 3], ro[0, 1, 3], bo[0, 1, 3] = 0, 0, 0
+        close(o, ro, bo, "the other rows")
+
+
 def test_tree_bad_values_are_flagged_and_contained():
     dims, L = D(T=6, B=3), 200
     x = _cache_inputs(dims, L, 19)
