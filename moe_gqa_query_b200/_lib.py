@@ -285,13 +285,12 @@ def _dev(t, name, dtype, dev, optional=False):
     than the current one, dev (the library launches on the current device)."""
     if t is None and optional:
         return None
-    if not isinstance(t, torch.Tensor):
-        return _ptr(t, name)
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        _ptr(t, name, dtype)
-    if t.get_device() != dev:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    p = _ptr(t, name, dtype)
+    if isinstance(t, torch.Tensor):
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    return t.data_ptr()
+    return p
 
 
 def _scratch(ws, dev):

@@ -21,7 +21,10 @@
 // in attn_bwd.cu.
 //
 // CTA: 512 threads, roles, tensor memory and barriers as in attn_bwd.cu, with
-// every ring counted over the whole stretch.  d = 64 keeps two key tiles' K and
+// every ring counted over the whole stretch, but for d = 128: dK reads dS from
+// shared memory there, so S^T(i+1) waits only for dV(i), and the drain warps
+// take a whole dQ row into registers, so dP^T(i+1) (over dQ(i)'s columns) waits
+// less.  d = 64 keeps two key tiles' K and
 // V in shared memory; d = 128 has room for one.  Tensor memory holds one dK and
 // one dV: the next key tile's first products into them wait until the drain
 // warps have read them (acc_free).
@@ -71,13 +74,11 @@ struct BwdWinCfg {
   static constexpr int OffDelta = OffLse + 2 * 512;             // [2][128] f32
   static constexpr int OffBar = OffDelta + 2 * 512;
   static constexpr size_t Smem = 1024 + OffBar + sizeof(BwdWinBarriers);
-  // tensor-memory columns of P^T and dS^T, by 16-query k-step and by warpgroup
+  // tensor-memory columns of P^T and (d = 64) dS^T, by 16-query k-step and by warpgroup
   static __device__ __forceinline__ uint32_t pt_col(int ks) { return kWide ? kS + ks * 8 : kPT + ks * 8; }
-  static __device__ __forceinline__ uint32_t dst_col(int ks) {
-    return kWide ? kS + 64 + ks * 8 : kDP + (ks >> 2) * 64 + (ks & 3) * 8;
-  }
+  static __device__ __forceinline__ uint32_t dst_col(int ks) { return kDP + (ks >> 2) * 64 + (ks & 3) * 8; }
   static __device__ __forceinline__ uint32_t pt_wcol(int w) { return kWide ? kS + 32 * w : kPT + 32 * w; }
-  static __device__ __forceinline__ uint32_t dst_wcol(int w) { return kWide ? kS + 64 + 32 * w : kDP + 64 * w; }
+  static __device__ __forceinline__ uint32_t dst_wcol(int w) { return kDP + 64 * w; }
 };
 
 // Query tiles (routed, then shared) that key tile jt of a group sees.
@@ -171,6 +172,14 @@ __device__ __forceinline__ void product_ts(uint32_t acc, uint32_t a0, uint32_t a
 #pragma unroll
   for (int ks = 0; ks < kTileW / 16; ++ks)
     umma_ts(acc, (ks < 4 ? a0 : a1) + (ks & 3) * 8, sdesc_at(db, ks * 2048), idesc, accumulate || ks > 0);
+}
+// A K-major and B MN-major in shared memory (dK at d = 128).
+__device__ __forceinline__ void product_km(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+  const uint64_t da = sdesc_sw128(a, 16, 1024), db = sdesc_sw128(b, kBoxW, 1024);
+#pragma unroll
+  for (int ks = 0; ks < kTileW / 16; ++ks)
+    umma_ss(acc, sdesc_at(da, (ks >> 2) * kBoxW + (ks & 3) * 32), sdesc_at(db, ks * 2048), idesc,
+            accumulate || ks > 0);
 }
 // Both operands MN-major in shared memory (dQ).
 __device__ __forceinline__ void product_mm(uint32_t acc, uint32_t a, uint32_t b, uint32_t idesc) {
@@ -278,9 +287,11 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
   Stretch c;
   c.start(p, sched);
 
-  // registers per thread: 96 x 128 + 144 x 256 + 128 x 128 = the launch's 512 x 128
+  // registers per thread, adding up to the launch's 512 x 128: issue, softmax and
+  // drain warps 96 x 128 + 144 x 256 + 128 x 128; at d = 128, where a drain warp
+  // holds a whole dQ row, 80 x 128 + 136 x 256 + 160 x 128
   if (warp < 4) {
-    set_regs_down<96>();
+    set_regs_down<C::kWide ? 80 : 96>();
     auto wait_w = [&](uint64_t* b, uint32_t parity) { return mbar_wait_warp(b, parity & 1, abort); };
     const bool leader = elect_one();
     if (warp == 0) {
@@ -368,9 +379,8 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
           }
           if (!more) break;
           // d = 64: dP^T(N+1) overwrites dS^T(N).  d = 128: S^T(N+1) overwrites
-          // P^T(N) and dS^T(N), dP^T(N+1) overwrites dQ(N)
-          if (C::kWide && !wait_w(&bar->pv_done, N)) break;
-          if (!wait_w(&bar->dk_done, N)) break;
+          // P^T(N), dP^T(N+1) overwrites dQ(N)
+          if (!wait_w(C::kWide ? &bar->pv_done : &bar->dk_done, N)) break;
         }
         if (C::kWide) {
           if (!issue_s(nx, N + 1)) break;
@@ -397,28 +407,45 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
       do {
         const int b = c.item % C::KVB;
         if (!wait_w(&bar->ds_full, N)) break;
-        if (c.first() && c.item > 0 && !wait_w(&bar->acc_free, c.item - 1)) break;
         tc_fence_after();
-        if (leader) {
-          product_ts(tmem + C::kDK, tmem + C::dst_col(0), tmem + C::dst_col(4),
-                     smem_u32(smem + C::OffQ + (N & 1) * C::TileBytes), idesc_k, !c.first());
-          umma_commit(&bar->q_empty[N & 1]);
-          umma_commit(&bar->dk_done);      // dS^T(N) has been read from tensor memory
+        const uint32_t q0 = smem_u32(smem + C::OffQ + (N & 1) * C::TileBytes);
+        const uint32_t k0 = smem_u32(smem + C::OffK + b * C::TileBytes);
+        if (C::kWide) {
+          // dQ first: its drain is what dP^T(N+1) waits for (dQ sits over dP^T's
+          // columns, which the warpgroups have read, ds_full)
+          if (leader) {
+            product_mm(tmem + C::kDQ, smem_u32(sDS), k0, idesc_q);
+            umma_commit(&bar->dq_full);
+          }
+          if (c.first() && c.item > 0 && !wait_w(&bar->acc_free, c.item - 1)) break;
+          tc_fence_after();
+          if (leader) {
+            product_km(tmem + C::kDK, smem_u32(sDS), q0, idesc_k, !c.first());
+            umma_commit(&bar->q_empty[N & 1]);
+            umma_commit(&bar->dk_done);
+          }
+        } else {
+          if (c.first() && c.item > 0 && !wait_w(&bar->acc_free, c.item - 1)) break;
+          tc_fence_after();
+          if (leader) {
+            product_ts(tmem + C::kDK, tmem + C::dst_col(0), tmem + C::dst_col(4), q0, idesc_k, !c.first());
+            umma_commit(&bar->q_empty[N & 1]);
+            umma_commit(&bar->dk_done);      // dS^T(N) has been read from tensor memory
+          }
+          // dQ(N) over dQ(N-1): wait for its drain
+          if (N >= 1 && !wait_w(&bar->dq_free, N - 1)) break;
+          tc_fence_after();
+          if (leader) {
+            product_mm(tmem + C::kDQ, smem_u32(sDS), k0, idesc_q);
+            umma_commit(&bar->dq_full);
+          }
         }
-        // dQ(N) over dQ(N-1): wait for its drain (d = 128: dQ sits over dP^T's
-        // columns, which the warpgroups have read, ds_full)
-        if (!C::kWide && N >= 1 && !wait_w(&bar->dq_free, N - 1)) break;
-        tc_fence_after();
-        if (leader) {
-          product_mm(tmem + C::kDQ, smem_u32(sDS), smem_u32(smem + C::OffK + b * C::TileBytes), idesc_q);
-          umma_commit(&bar->dq_full);
-          if (c.last()) umma_commit(&bar->k_empty[b]);
-        }
+        if (leader && c.last()) umma_commit(&bar->k_empty[b]);
         ++N;
       } while (c.next(p));
     }
   } else if (warp < 12) {
-    set_regs_up<144>();
+    set_regs_up<C::kWide ? 136 : 144>();
     // ---------------- P and dS: one key row per thread, 64 query columns per warpgroup
     const int wg = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;
@@ -515,12 +542,12 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
             dsk[c4 * 2 + e / 2] = pack_bf16x2(a0, a1);
           }
         }
-        // dS^T row r for dK: into this warpgroup's tensor-memory columns ...
-        tmem_st16(tmem + lane_off + C::dst_wcol(wg) + ch * 16, dsk);
-        // ... and for dQ into the MN-major smem operand (the 64-query atom of this
-        // warpgroup, 16-byte pieces swizzled by key row), once dQ(N-1) has read
-        // the previous tile's (d = 128: dP^T(N) was issued after that)
-        if (!C::kWide && ch == 0 && N > 0) ok = wait(&bar->dq_full, N - 1);
+        // d = 64: dS^T row r for dK into this warpgroup's tensor-memory columns
+        if (!C::kWide) tmem_st16(tmem + lane_off + C::dst_wcol(wg) + ch * 16, dsk);
+        // for dQ (MN-major) and, at d = 128, dK (K-major) into shared memory: the
+        // 64-query atom of this warpgroup, 16-byte pieces swizzled by key row, once
+        // the last products have read the previous tile's (the second of dQ and dK)
+        if (ch == 0 && N > 0) ok = wait(C::kWide ? &bar->dk_done : &bar->dq_full, N - 1);
         if (!ok) break;
         uint8_t* atom = sDS + wg * kBoxW + r * 128;
 #pragma unroll
@@ -529,7 +556,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
                        dsk[j * 4 + 3]);
       }
       if (!ok) break;
-      tmem_wait_st();
+      if (!C::kWide) tmem_wait_st();
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(&bar->ds_full);
@@ -537,6 +564,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
       ++N;
     } while (c.next(p));
   } else {
+    if (C::kWide) set_regs_up<160>();
     // ---------------- dQ drain (TMA reduce-add into fp32); dK, dV at the end of each key tile
     const int qd = warp & 3;
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
@@ -558,6 +586,12 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         if (!wait(&bar->dq_full, N)) goto out;
         tc_fence_after();
         const int row_pad = c.row_pad(p);
+        // the whole row at once, so that the columns are free again soon (d = 128:
+        // dP^T(N+1) waits for them)
+        uint32_t v[D];
+        tmem_ld<D>(tmem + lane_off + C::kDQ, v);
+        tc_fence_before();
+        mbar_arrive(&bar->dq_free);
 #pragma unroll
         for (int g0 = 0; g0 < D / 32; g0 += C::EpiCh) {
           // staging free: every earlier reduce of this warp has read it
@@ -565,16 +599,11 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < C::EpiCh; ++i) {
-            uint32_t v[32];
-            tmem_ld32(tmem + lane_off + C::kDQ + (g0 + i) * 32, v);
-            if (g0 + i == D / 32 - 1) {
-              tc_fence_before();
-              mbar_arrive(&bar->dq_free);
-            }
+            const uint32_t* w = v + (g0 + i) * 32;
             uint8_t* rowp = stage + i * 4096 + lane * 128;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              st_shared_v4(rowp + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              st_shared_v4(rowp + ((j ^ (lane & 7)) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
           }
           fence_proxy_async_smem();
           __syncwarp();

@@ -103,24 +103,6 @@ __device__ __forceinline__ CacheList cache_list(const CacheAttnParams& p, int b)
   return c;
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t* r) {
-  if constexpr (N == 16) tmem_ld16(a, r);
-  else if constexpr (N == 32) tmem_ld32(a, r);
-  else if constexpr (N == 64) tmem_ld64(a, r);
-  else tmem_ld128(a, r);
-}
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t* r) {
-  if constexpr (N == 8) tmem_st8(a, r);
-  else if constexpr (N == 16) tmem_st16(a, r);
-  else if constexpr (N == 32) tmem_st32(a, r);
-  else {
-    tmem_st32(a, r);
-    tmem_st32(a + 32, r + 32);
-  }
-}
-
 struct RowState {
   float m, l;
   bool ok;

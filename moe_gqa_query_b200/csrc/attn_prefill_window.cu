@@ -82,9 +82,7 @@ __device__ __forceinline__ void softmax_tile(RowTile& st, PrefillWinBarriers* ba
   constexpr int NH = C::kHalves && NC == 128 ? 2 : 1;      // P in halves
   const float sl2 = p.scale_log2;
   uint32_t s[NC];
-  if constexpr (NC == 128) tmem_ld128(lane_base + C::kS, s);
-  else if constexpr (NC == 64) tmem_ld64(lane_base + C::kS, s);
-  else tmem_ld32(lane_base + C::kS, s);
+  tmem_ld<NC>(lane_base + C::kS, s);
   tc_fence_before();
   mbar_arrive(&bar->s_free);       // S(j) is in registers
   if (diag || border) {
@@ -159,8 +157,7 @@ __device__ __forceinline__ void softmax_tile(RowTile& st, PrefillWinBarriers* ba
         }
       }
     }
-    if constexpr (PC == 32) tmem_st32(lane_base + C::kP + h * PC, pk);
-    else tmem_st16(lane_base + C::kP + h * PC, pk);
+    tmem_st<PC>(lane_base + C::kP + h * PC, pk);
     tmem_wait_st();
     tc_fence_before();
     if (C::kHalves && h == 0) mbar_arrive(&bar->p_half);
