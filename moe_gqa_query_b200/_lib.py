@@ -155,11 +155,11 @@ def _ptr(t, name="tensor", dtype=None, optional=False):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         if _raw_stream is None:
             return torch.cuda.current_stream().cuda_stream
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -303,7 +303,7 @@ def gqe_attn_prefill_window(dims, q_routed, q_sh, K, V, window, sinks, o_routed,
     _check("gqe_attn_prefill_window", lib.gqe_attn_prefill_window(
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
         _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), int(window), int(sinks), _dev(o_routed, "o_routed", _BF16, dev),
-        _dev(o_sh, "o_sh", _BF16, dev, True), _dev(lse, "lse", _F32, dev, True), _stream(stream)))
+        _dev(o_sh, "o_sh", _BF16, dev, True), _dev(lse, "lse", _F32, dev, True), _stream(stream, dev)))
 
 
 def gqe_attn_prefill_window_bwd(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, do_routed, do_sh,
@@ -316,7 +316,7 @@ def gqe_attn_prefill_window_bwd(dims, q_routed, q_sh, K, V, window, sinks, o_rou
         _dev(o_sh, "o_sh", _BF16, dev, True), _dev(lse, "lse", _F32, dev), _dev(do_routed, "do_routed", _BF16, dev),
         _dev(do_sh, "do_sh", _BF16, dev, True), _dev(dq_routed, "dq_routed", _BF16, dev),
         _dev(dq_sh, "dq_sh", _BF16, dev, True), _dev(dK, "dK", _BF16, dev), _dev(dV, "dV", _BF16, dev), wp, ws_bytes,
-        _stream(stream)))
+        _stream(stream, dev)))
 
 
 def gqe_attn_decode_window(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, window, sinks, o_routed, o_sh, ws=None,
@@ -325,9 +325,9 @@ def gqe_attn_decode_window(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, windo
     wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_decode_window", lib.gqe_attn_decode_window(
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
-        _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max), _dev(cache_len, "cache_len", _I32, dev), int(window),
-        int(sinks), _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes,
-        _stream(stream)))
+        _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max),
+        _dev(cache_len, "cache_len", _I32, dev), int(window), int(sinks), _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes,
+        _stream(stream, dev)))
 
 
 def gqe_attn_tree(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max, cache_len, window, sinks, o_routed,
@@ -337,10 +337,11 @@ def gqe_attn_tree(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max,
     dev = torch.cuda.current_device()
     wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_tree", lib.gqe_attn_tree(
-        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True), _dev(Kt, "Kt", _BF16, dev),
-        _dev(Vt, "Vt", _BF16, dev), _dev(parent, "parent", _I32, dev), _dev(tree_len, "tree_len", _I32, dev, True),
-        _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max), _dev(cache_len, "cache_len", _I32, dev), int(window), int(sinks),
-        _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes, _stream(stream)))
+        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
+        _dev(Kt, "Kt", _BF16, dev), _dev(Vt, "Vt", _BF16, dev), _dev(parent, "parent", _I32, dev),
+        _dev(tree_len, "tree_len", _I32, dev, True), _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev),
+        int(L_max), _dev(cache_len, "cache_len", _I32, dev), int(window), int(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes, _stream(stream, dev)))
 
 
 def gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, L_max, cache_len, new_len, stream=None):
@@ -350,7 +351,7 @@ def gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, L_max, cache_len, new
     _check("gqe_cache_commit", lib.gqe_cache_commit(
         ctypes.byref(dims), _dev(Kt, "Kt", _BF16, dev), _dev(Vt, "Vt", _BF16, dev), _dev(path, "path", _I32, dev),
         _dev(n_accept, "n_accept", _I32, dev), _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max),
-        _dev(cache_len, "cache_len", _I32, dev), _dev(new_len, "new_len", _I32, dev), _stream(stream)))
+        _dev(cache_len, "cache_len", _I32, dev), _dev(new_len, "new_len", _I32, dev), _stream(stream, dev)))
 
 
 def gqe_combine(dims, o_routed, o_sh, topk_w, h, stream=None):
