@@ -30,8 +30,8 @@ cudaError_t launch_attn_prefill(const CUtensorMap& mQ, const CUtensorMap& mQs, c
                                 const CUtensorMap& mV, const AttnParams& p, int d,
                                 cudaStream_t stream);
 // The same attention under a sliding window with sinks (p.window, p.sinks);
-// the K and V maps' boxes hold attn_window_key_tile(d) rows.
-constexpr int attn_window_key_tile(int d) { return d == 64 ? 128 : 64; }
+// the K and V maps' boxes hold kWindowKeyTile rows.
+constexpr int kWindowKeyTile = 64;
 cudaError_t launch_attn_prefill_window(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
                                        const CUtensorMap& mV, const AttnParams& p, int d, cudaStream_t stream);
 
@@ -136,7 +136,8 @@ struct CacheAttnPlan {
 
 void cache_attn_plan(int B, int T, int G, int k, int n_shared, int d, int L_max, bool tree, int window, int sinks,
                      CacheAttnPlan* P);
-// (the K and V maps' boxes hold attn_window_key_tile(d) rows)
+// Key rows per box of the K and V maps.
+constexpr int cache_attn_key_tile(int d) { return d == 64 ? 128 : 64; }
 cudaError_t launch_attn_cache(const CUtensorMap& mK, const CUtensorMap& mV, const CUtensorMap& mKt,
                               const CUtensorMap& mVt, const CacheAttnParams& p, int d, long long items,
                               cudaStream_t stream);

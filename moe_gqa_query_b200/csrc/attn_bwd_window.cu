@@ -648,6 +648,7 @@ __device__ __forceinline__ void join_walk(const AttnBwdParams& p, const AttnBwdS
     if (kv_pos >= p.T) continue;
     const size_t at = ((size_t)which * kTileW + row) * p.d + c4 * 4;
     float4 a = *reinterpret_cast<const float4*>(p.part + (size_t)(2 * (c - 1) + 1) * slot + at);
+#pragma unroll 4
     for (int i = c; i <= last; ++i) {
       const float4 x = *reinterpret_cast<const float4*>(p.part + (size_t)(2 * i) * slot + at);
       a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;

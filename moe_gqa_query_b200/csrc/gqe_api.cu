@@ -440,7 +440,7 @@ static gqe_status prefill_common(const gqe_dims* dims, const gqe_bf16* q_routed,
   if (dims->n_shared) GQE_REQUIRE(map3d(&mQs, q_sh, d, T, B, 128), GQE_ERR_CUDA);
   else mQs = mQ;
   const bool win = has_window(dims, window);
-  const uint32_t box = win ? attn_window_key_tile(d) : 128;
+  const uint32_t box = win ? kWindowKeyTile : 128;
   GQE_REQUIRE(map3d(&mK, K, d, T, (uint64_t)B * G, box), GQE_ERR_CUDA);
   GQE_REQUIRE(map3d(&mV, V, d, T, (uint64_t)B * G, box), GQE_ERR_CUDA);
   AttnParams p{};
@@ -594,7 +594,7 @@ static gqe_status cache_attn_common(const gqe_dims* dims, const gqe_bf16* q_rout
   (void)ws;            // the shares are joined on chip: no scratch (gqe_window_workspace_size says 0)
   (void)ws_bytes;
   GQE_REQUIRE(P.items <= 0x7FFFFFFFll, GQE_ERR_UNSUPPORTED);
-  const uint32_t box = attn_window_key_tile(d);
+  const uint32_t box = cache_attn_key_tile(d);
   CUtensorMap mK, mV, mKt, mVt;
   GQE_REQUIRE(map3d(&mK, Kc, d, L_max, (uint64_t)B * G, box), GQE_ERR_CUDA);
   GQE_REQUIRE(map3d(&mV, Vc, d, L_max, (uint64_t)B * G, box), GQE_ERR_CUDA);
