@@ -196,8 +196,10 @@ gqe_status gqe_attn_prefill_window(const gqe_dims* dims, const gqe_bf16* q_route
 
 /* Backward of gqe_attn_prefill_window for the same window and sinks; the other
  * arguments are those of gqe_attn_prefill_bwd (o and lse from
- * gqe_attn_prefill_window).  dK and dV do not depend on timing; dq is summed
- * over key tiles in an order that may differ between runs.
+ * gqe_attn_prefill_window).  Delta is taken from P and dP in fp32, not from O
+ * (which is rounded), for rows that see at most 16 keys.  dK and dV do not
+ * depend on timing; dq is summed over key tiles in an order that may differ
+ * between runs.
  *   ws: gqe_window_workspace_size(GQE_OP_ATTN_WINDOW_BWD) bytes, 256-byte
  *   aligned. */
 gqe_status gqe_attn_prefill_window_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
@@ -262,7 +264,8 @@ gqe_status gqe_cache_commit(const gqe_dims* dims, const gqe_bf16* Kt, const gqe_
 
 /* Bytes of scratch of the windowed and tree calls: op GQE_OP_ATTN_WINDOW_BWD,
  * GQE_OP_ATTN_DECODE_WINDOW (dims->T = 1) or GQE_OP_ATTN_TREE, L_max the cache
- * length (the last two).  May be 0.  Errors as the calls themselves. */
+ * length (the last two).  May be 0 (it is for the last two: their partial
+ * states stay on chip).  Errors as the calls themselves. */
 gqe_status gqe_window_workspace_size(const gqe_dims* dims, int op, int L_max, int window, int sinks, size_t* bytes);
 
 /* C [M, N] = sum_k A(m, k) B(n, k), bf16 in and out, fp32 accumulation on

@@ -76,6 +76,10 @@ struct AttnBwdParams {
   unsigned* err;
   // windowed launches only: 1 <= window <= T, 0 <= sinks <= T
   int window, sinks;
+  const gqe_bf16_t* q_routed;       // the forward's inputs (rows that see few keys)
+  const gqe_bf16_t* q_sh;
+  const gqe_bf16_t* K;
+  const gqe_bf16_t* V;
   float* part;                      // cut walks' sums: [2 * CTAs, 2 (dK, dV), 128, d] fp32
 };
 
@@ -85,7 +89,6 @@ struct AttnBwdLayout {
   size_t off_lse2, off_delta, off_dq, bytes;
 };
 
-cudaError_t launch_attn_bwd_prep(const AttnBwdParams& p, cudaStream_t stream);
 
 // Windowed backward (attn_bwd_window.cu): where each CTA starts in the list of
 // (sequence, key tile, query tile of its walk), cut into equal stretches.

@@ -580,9 +580,8 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(AttnBwdParams p) {
   acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
   acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (part == 0) {
-    const float sgn = p.window ? -1.f : 1.f;       // the windowed kernel adds both
-    p.delta[pr] = valid ? dot * sgn : 0.f;
-    p.lse2[pr] = (valid ? p.lse[src] * 1.4426950408889634f : INFINITY) * sgn;
+    p.delta[pr] = valid ? dot : 0.f;
+    p.lse2[pr] = valid ? p.lse[src] * 1.4426950408889634f : INFINITY;
   }
 }
 
@@ -630,18 +629,13 @@ void attn_bwd_layout(int B, int T, int G, int k, int n_shared, int d, AttnBwdLay
   L->bytes = o;
 }
 
-cudaError_t launch_attn_bwd_prep(const AttnBwdParams& p, cudaStream_t stream) {
-  const long long threads = p.n_rows_pad * (p.d / 8);
-  return launch_kernel(attn_bwd_prep_kernel, dim3((int)((threads + 255) / 256)), dim3(256), 0, stream, 1, p);
-}
-
 cudaError_t launch_attn_bwd(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mdO,
                             const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
                             const CUtensorMap& mdQ, const AttnBwdParams& p, cudaStream_t stream) {
   if (p.d != 64 && p.d != 128) return cudaErrorNotSupported;
   const long long threads = p.n_rows_pad * (p.d / 8);
   const int blocks = (int)((threads + 255) / 256);
-  cudaError_t e = launch_attn_bwd_prep(p, stream);
+  cudaError_t e = launch_kernel(attn_bwd_prep_kernel, dim3(blocks), dim3(256), 0, stream, 1, p);
   if (e != cudaSuccess) return e;
   auto kern = p.d == 64 ? attn_bwd_kernel<64> : attn_bwd_kernel<128>;
   const size_t smem = p.d == 64 ? BwdCfg<64>::Smem : BwdCfg<128>::Smem;

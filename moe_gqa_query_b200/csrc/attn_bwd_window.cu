@@ -29,6 +29,13 @@
 // one dV: the next key tile's first products into them wait until the drain
 // warps have read them (acc_free).
 //
+// Delta = dO . O takes the forward's O, which is rounded to bf16.  The error is
+// |dO||O| 2^-9 a row, next to |dO||V - O| in dP - Delta: of no account when O
+// averages many keys, but as large as all other roundings together for a row
+// that sees two or three (dq of 3-token sequences 0.0039 off, norm-wise, against
+// 0.0018 in fp32).  Rows that see at most kFewKeys keys take Delta = sum_j P_j
+// dP_j in fp32 instead, in the prep kernel.
+//
 // P and dS are computed with packed pairs (f32x2): the prep kernel stores -LSE2
 // and -Delta, so a pair costs one FMA before its exponentials and one add and
 // one multiply after them; the scale of dS moves to where dK and dq are rounded.
@@ -42,6 +49,7 @@ namespace gqe {
 namespace {
 
 constexpr int kThreadsW = 512;
+constexpr int kFewKeys = 16;
 constexpr int kTileW = 128;
 constexpr int kBoxW = 128 * 64 * 2;   // one 128-row x 64-column bf16 TMA box
 
@@ -630,6 +638,68 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
   drain_after_abort(abort);
 }
 
+__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
+  const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+  float d = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d += bf16_lo(av[e]) * bf16_lo(bv[e]) + bf16_hi(av[e]) * bf16_hi(bv[e]);
+  return d;
+}
+
+// -Delta and -LSE2 of every row of the padded row space (LSE2 +inf and Delta 0
+// on padding rows, so their P is 0), and the dQ accumulator zeroed.  d/8 threads
+// a row, 16 bytes each; HBM-bound (o, dO, the accumulator).
+__global__ void __launch_bounds__(256) attn_bwd_window_prep_kernel(const __grid_constant__ AttnBwdParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tpr = p.d / 8;
+  const long long gt = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long pr = gt / tpr;
+  const int part = (int)(gt % tpr);
+  if (pr >= p.n_rows_pad) return;      // whole rows: tpr divides 32
+  const unsigned row_lanes = (tpr == 8 ? 0xFFu : 0xFFFFu) << (threadIdx.x & 31 & ~(tpr - 1));
+  const int BG = p.B * p.G;
+  const long long routed_rows = (long long)BG * p.rows_pad;
+  const bool shared = pr >= routed_rows;
+  const long long q2 = shared ? pr - routed_rows : pr;
+  const int pad = shared ? p.rows_pad_sh : p.rows_pad, kk = shared ? 1 : p.k;
+  const int sq = (int)(q2 / pad), r = (int)(q2 - (long long)sq * pad);       // sequence (or batch entry), row in it
+  const bool valid = r < p.T * kk;
+  const long long src = (long long)sq * p.T * kk + r;
+  const gqe_bf16_t* o = (shared ? p.o_sh : p.o_routed) + src * p.d;
+  const gqe_bf16_t* dO = (shared ? p.do_sh : p.do_routed) + src * p.d;
+  float lse2 = INFINITY, delta = 0.f;
+  if (valid) {
+    lse2 = p.lse[shared ? (long long)BG * p.T * p.k + src : src] * 1.4426950408889634f;
+    const uint4 dov = reinterpret_cast<const uint4*>(dO)[part];
+    const int t = r / kk, lo = max(0, t - p.window + 1), first = min(p.sinks, lo), n = first + t - lo + 1;
+    if (n <= kFewKeys) {
+      const uint4 qv = reinterpret_cast<const uint4*>((shared ? p.q_sh : p.q_routed) + src * p.d)[part];
+      const size_t kv0 = (size_t)(shared ? sq * p.G + p.sg : sq) * p.T * tpr + part;
+      for (int j = 0; j < n; ++j) {
+        const size_t at = kv0 + (size_t)(j < first ? j : lo + j - first) * tpr;
+        float s = dot8(qv, reinterpret_cast<const uint4*>(p.K)[at]);
+        float dp = dot8(dov, reinterpret_cast<const uint4*>(p.V)[at]);
+        for (int off = tpr >> 1; off > 0; off >>= 1) {
+          s += __shfl_xor_sync(row_lanes, s, off);
+          dp += __shfl_xor_sync(row_lanes, dp, off);
+        }
+        delta = fmaf(ex2(fmaf(s, p.scale_log2, -lse2)), dp, delta);
+      }
+    } else {
+      delta = dot8(reinterpret_cast<const uint4*>(o)[part], dov);
+      for (int off = tpr >> 1; off > 0; off >>= 1) delta += __shfl_xor_sync(row_lanes, delta, off);
+    }
+  }
+  float4* acc = reinterpret_cast<float4*>(p.dq_acc + pr * p.d + part * 8);
+  acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+  acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (part == 0) {
+    p.delta[pr] = -delta;
+    p.lse2[pr] = -lse2;
+  }
+}
+
 // dK, dV of a walk that the stretches' ends cut: the pieces of the walk cut
 // between CTAs c-1 and c added in their order, when that is the walk's first cut.
 // Each of the kJoinBlocks blocks takes its part of the tile.
@@ -758,13 +828,13 @@ cudaError_t launch_attn_bwd_window(const CUtensorMap& mQ, const CUtensorMap& mQs
                                    const CUtensorMap& mdOs, const CUtensorMap& mK, const CUtensorMap& mV,
                                    const CUtensorMap& mdQ, const AttnBwdParams& p, const AttnBwdSchedule& S,
                                    cudaStream_t stream) {
-  cudaError_t e = launch_attn_bwd_prep(p, stream);
+  const long long row_blocks = (p.n_rows_pad * (p.d / 8) + 255) / 256;
+  cudaError_t e = launch_kernel(attn_bwd_window_prep_kernel, dim3((unsigned)row_blocks), dim3(256), 0, stream, 1, p);
   if (e != cudaSuccess) return e;
   e = p.d == 64 ? launch_win<64>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S, stream)
                 : launch_win<128>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S, stream);
   if (e != cudaSuccess) return e;
-  const long long blocks = (p.n_rows_pad * (p.d / 8) + 255) / 256 + (S.n_ctas - 1) * kJoinBlocks;
-  return launch_kernel(attn_bwd_window_post_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, 1, p, S);
+  return launch_kernel(attn_bwd_window_post_kernel, dim3((unsigned)(row_blocks + (S.n_ctas - 1) * kJoinBlocks)), dim3(256), 0, stream, 1, p, S);
 }
 
 }  // namespace gqe

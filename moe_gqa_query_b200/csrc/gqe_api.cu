@@ -473,8 +473,10 @@ gqe_status gqe_attn_prefill_window(const gqe_dims* dims, const gqe_bf16* q_route
   return prefill_common(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, stream);
 }
 
+// win: the windowed backward, which runs without a bound too (window T), since
+// its Delta is more exact for tokens that see few keys.
 static gqe_status prefill_bwd_common(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
-                                     const gqe_bf16* K, const gqe_bf16* V, int window, int sinks,
+                                     const gqe_bf16* K, const gqe_bf16* V, bool win, int window, int sinks,
                                      const gqe_bf16* o_routed, const gqe_bf16* o_sh, const float* lse,
                                      const gqe_bf16* do_routed, const gqe_bf16* do_sh, gqe_bf16* dq_routed,
                                      gqe_bf16* dq_sh, gqe_bf16* dK, gqe_bf16* dV, void* ws, size_t ws_bytes,
@@ -492,7 +494,7 @@ static gqe_status prefill_bwd_common(const gqe_dims* dims, const gqe_bf16* q_rou
   const int B = dims->B, T = dims->T, G = dims->G, k = dims->k, d = dims->d_head;
   AttnBwdLayout L;
   attn_bwd_layout(B, T, G, k, dims->n_shared, d, &L);
-  const bool win = has_window(dims, window);
+  if (!has_window(dims, window)) window = T;
   const int n_sinks = sinks < T ? sinks : T;
   AttnBwdSchedule sched;
   size_t off_part = 0, need = L.bytes;
@@ -544,10 +546,14 @@ static gqe_status prefill_bwd_common(const gqe_dims* dims, const gqe_bf16* q_rou
   if (!win) return cuda_status(launch_attn_bwd(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S(stream)));
   p.window = window;
   p.sinks = n_sinks;
-  // a window of one token without sinks: every softmax is over one key, whose
-  // weight is 1 whatever its score, so dS is 0 (and not the rounding that
-  // dP - Delta would leave)
-  if (window == 1 && n_sinks == 0) p.scale = 0.f;
+  p.q_routed = q_routed;
+  p.q_sh = q_sh;
+  p.K = K;
+  p.V = V;
+  // a window of one token without sinks (or a sequence of one): every softmax is
+  // over one key, whose weight is 1 whatever its score, so dS is 0 (and not the
+  // rounding that dP - Delta would leave)
+  if (T == 1 || (window == 1 && n_sinks == 0)) p.scale = 0.f;
   p.part = reinterpret_cast<float*>(w + off_part);
   return cuda_status(launch_attn_bwd_window(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, sched, S(stream)));
 }
@@ -557,7 +563,7 @@ gqe_status gqe_attn_prefill_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, 
                                 const gqe_bf16* o_sh, const float* lse, const gqe_bf16* do_routed,
                                 const gqe_bf16* do_sh, gqe_bf16* dq_routed, gqe_bf16* dq_sh, gqe_bf16* dK,
                                 gqe_bf16* dV, void* ws, size_t ws_bytes, gqe_stream stream) {
-  return prefill_bwd_common(dims, q_routed, q_sh, K, V, 0, 0, o_routed, o_sh, lse, do_routed, do_sh, dq_routed, dq_sh,
+  return prefill_bwd_common(dims, q_routed, q_sh, K, V, false, 0, 0, o_routed, o_sh, lse, do_routed, do_sh, dq_routed, dq_sh,
                             dK, dV, ws, ws_bytes, stream);
 }
 
@@ -567,7 +573,7 @@ gqe_status gqe_attn_prefill_window_bwd(const gqe_dims* dims, const gqe_bf16* q_r
                                        const gqe_bf16* do_routed, const gqe_bf16* do_sh, gqe_bf16* dq_routed,
                                        gqe_bf16* dq_sh, gqe_bf16* dK, gqe_bf16* dV, void* ws, size_t ws_bytes,
                                        gqe_stream stream) {
-  return prefill_bwd_common(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, do_routed, do_sh,
+  return prefill_bwd_common(dims, q_routed, q_sh, K, V, true, window, sinks, o_routed, o_sh, lse, do_routed, do_sh,
                             dq_routed, dq_sh, dK, dV, ws, ws_bytes, stream);
 }
 
@@ -677,11 +683,10 @@ gqe_status gqe_window_workspace_size(const gqe_dims* dims, int op, int L_max, in
   GQE_REQUIRE(bytes && window >= 0 && sinks >= 0, GQE_ERR_INVALID_ARG);
   const int B = dims->B, T = dims->T, G = dims->G, k = dims->k, d = dims->d_head;
   if (op == GQE_OP_ATTN_WINDOW_BWD) {
-    if (!has_window(dims, window)) return gqe_workspace_size(dims, GQE_OP_ATTN_BWD, 0, bytes);
     AttnBwdSchedule sched;
     size_t off_part;
-    attn_bwd_window_plan(B, T, G, k, dims->n_shared, dims->shared_kv_group, d, window, sinks < T ? sinks : T, &sched,
-                         &off_part, bytes);
+    attn_bwd_window_plan(B, T, G, k, dims->n_shared, dims->shared_kv_group, d, has_window(dims, window) ? window : T,
+                         sinks < T ? sinks : T, &sched, &off_part, bytes);
     return GQE_OK;
   }
   if (op == GQE_OP_ATTN_DECODE_WINDOW || op == GQE_OP_ATTN_TREE) {

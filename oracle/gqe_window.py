@@ -79,23 +79,33 @@ def masked_attention_error_bound(q, vis, K, V, scale):
     return out
 
 
-def masked_attention_bwd(q, vis, K, V, dO, scale, O, lse):
+FEW_KEYS = 16       # rows that see at most this many keys have their Delta from P and dP (see below)
+
+
+def masked_attention_bwd(q, vis, K, V, dO, scale, lse):
     """Gradients of masked_attention: with P = exp(S - lse) on visible keys,
-    dV = P^T dO, dS = P (dO V^T - Delta), Delta = dO . O, dq = scale dS K,
-    dK = scale dS^T q; and the worst-case errors of the three computed as the
-    tensor cores do it (P and dS rounded to bf16, fp32 sums; see
-    causal_attention_bwd_error_bound, plus 1e-4 for the exponential).
+    dP = dO V^T, Delta = sum_j P_j dP_j, dS = P (dP - Delta): dV = P^T dO,
+    dq = scale dS K, dK = scale dS^T q.
+
+    And the worst-case errors of the three computed as the tensor cores do it
+    (P and dS rounded to bf16, fp32 sums; see causal_attention_bwd_error_bound,
+    plus 1e-4 for the exponential).  Delta may come from dO . O with O rounded
+    to bf16, 2^-8 sum|dO||O| off, for rows that see more than FEW_KEYS keys.
     Returns (dq, dK, dV), (bound_dq, bound_dK, bound_dV)."""
-    q, K, V, dO, O = f64(q), f64(K), f64(V), f64(dO), f64(O)
+    q, K, V, dO = f64(q), f64(K), f64(V), f64(dO)
     P = np.where(vis, np.exp(np.where(vis, q @ K.T * scale, -np.inf) - np.asarray(lse)[:, None]), 0.0)
     dP = dO @ V.T
-    delta = (dO * O).sum(1, keepdims=True)
+    delta = (P * dP).sum(1, keepdims=True)
     dS = P * (dP - delta)
     d, L, R = q.shape[1], K.shape[0], q.shape[0]
     gd, gL, gR = d * U_FP32, L * U_FP32, R * U_FP32
     aq, aK, aV, aO = np.abs(q), np.abs(K), np.abs(V), np.abs(dO)
-    eP = P * (scale * gd * (aq @ aK.T) + 1e-4)
-    edS = scale * (np.abs(dP - delta) * eP + P * gd * (aO @ aV.T + (aO * np.abs(O)).sum(1, keepdims=True)))
+    eE = scale * gd * (aq @ aK.T) + 1e-4
+    eP = P * eE
+    adOO = (aO * np.abs(P @ V)).sum(1, keepdims=True)
+    few = vis.sum(1, keepdims=True) <= FEW_KEYS
+    e_delta = np.where(few, (P * eE * np.abs(dP)).sum(1, keepdims=True), U_BF16 * adOO)
+    edS = scale * (np.abs(dP - delta) * eP + P * (e_delta + gd * (aO @ aV.T + adOO)))
     aS = np.abs(scale * dS)
     bounds = (((U_BF16 + gL) * aS + edS) @ aK, ((U_BF16 + gR) * aS + edS).T @ aq,
               ((U_BF16 + gR) * P + eP).T @ aO)
@@ -134,21 +144,18 @@ def attn_prefill_window(q_routed, q_sh, K, V, dims, window, sinks):
     return (o, os_ if dims.n_shared else None, flat), (e, es if dims.n_shared else None)
 
 
-def attn_prefill_window_bwd(q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, do_routed, do_sh, dims):
-    """(dq_routed, dq_sh, dK, dV) and their error bounds, from the forward's O
-    and lse (library layout)."""
+def attn_prefill_window_bwd(q_routed, q_sh, K, V, window, sinks, lse, do_routed, do_sh, dims):
+    """(dq_routed, dq_sh, dK, dV) and their error bounds, from the forward's lse
+    (library layout)."""
     B, T, G, k, d = dims.B, dims.T, dims.G, dims.k, dims.d
     sc = attention_scale(dims)
     out = [np.zeros((B, G, T, k, d)), np.zeros((B, T, d)), np.zeros((B, G, T, d)), np.zeros((B, G, T, d))]
     bnd = [np.zeros_like(x) for x in out]
     for b, g, sh, tok, rows in _row_sets(dims, T, q_routed, q_sh):
         vis = sees(tok[:, None], np.arange(T)[None], window, sinks)
-        if sh:
-            O, dO, l0 = o_sh[b], do_sh[b], B * G * T * k + b * T
-        else:
-            O, dO = np.asarray(o_routed[b, g]).reshape(T * k, d), np.asarray(do_routed[b, g]).reshape(T * k, d)
-            l0 = (b * G + g) * T * k
-        grads, bounds = masked_attention_bwd(rows, vis, K[b, g], V[b, g], dO, sc, O, lse[l0:l0 + len(tok)])
+        dO = do_sh[b] if sh else np.asarray(do_routed[b, g]).reshape(T * k, d)
+        l0 = B * G * T * k + b * T if sh else (b * G + g) * T * k
+        grads, bounds = masked_attention_bwd(rows, vis, K[b, g], V[b, g], dO, sc, lse[l0:l0 + len(tok)])
         for dst, (dq, dK, dV) in ((out, grads), (bnd, bounds)):
             if sh:
                 dst[1][b] = dq

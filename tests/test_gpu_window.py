@@ -132,7 +132,9 @@ def _run_bwd(dims, dev, window, sinks, o, os_, lse, do, dos):
 
 
 # few sequences: every stretch ends inside a walk, the sink tiles' walks span many; many sequences: most walks whole
-BWD = dict(PREFILL, split_one_sink=(D(T=5000, G=1), 300, 1), split_two_tiles=(D(T=4500, G=1, E=4, k=2, sg=0), 64, 200),
+BWD = dict(PREFILL, three_tokens=(D(T=3, B=4, G=1), 67, 0), ten_tokens=(D(T=10, B=2, G=4, sg=3), 594, 1),
+           two_keys=(D(T=300, k=2), 2, 0), few_keys_d128=(D(T=300, d=128), 9, 6), few_and_many=(D(T=300), 16, 1),
+           split_one_sink=(D(T=5000, G=1), 300, 1), split_two_tiles=(D(T=4500, G=1, E=4, k=2, sg=0), 64, 200),
            split_d128=(D(T=3000, G=1, E=4, k=2, d=128), 256, 5), sinks_unsplit=(D(B=8, T=2600, G=2, n_shared=0), 30, 2500))
 
 
@@ -152,8 +154,7 @@ def test_prefill_window_backward(case):
         dims = dims.replace(B=2)
         x = {n: None if v is None else v[keep] for n, v in x.items()}
         do, o, dq, dK, dV = do[keep], o[keep], dq[keep], dK[keep], dV[keep]
-    ref, bnd = ow.attn_prefill_window_bwd(x["q"], x["qs"], x["K"], x["V"], window, sinks, to_f64(o),
-                                          to_f64(os_) if dims.n_shared else None, to_f64(lse), do, dos, dims)
+    ref, bnd = ow.attn_prefill_window_bwd(x["q"], x["qs"], x["K"], x["V"], window, sinks, to_f64(lse), do, dos, dims)
     for name, got, r, b in zip(("dq", "dq_sh", "dK", "dV"), (dq, dqs, dK, dV), ref, bnd):
         if got is not None:
             close(got, r, b, name)
@@ -169,8 +170,9 @@ def test_window_backward_dK_dV_are_deterministic():
     assert torch.equal(a[2], b[2]) and torch.equal(a[3], b[3])
 
 
-def test_window_of_one_has_no_score_gradient():
-    dims, window, sinks = PREFILL["window_one"]
+@pytest.mark.parametrize("case", ["window_one", "one_token"])
+def test_one_visible_key_has_no_score_gradient(case):
+    dims, window, sinks = PREFILL[case]
     x = _prefill_inputs(dims, 15)
     dev, o, os_, lse = _run_prefill(dims, x, window, sinks)
     dq, dqs, dK, dV = _run_bwd(dims, dev, window, sinks, o, os_, lse, torch.ones_like(o), torch.ones_like(os_))

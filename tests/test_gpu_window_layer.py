@@ -59,7 +59,7 @@ def windowed(window, sinks):
 
     def bwd(q, qs, K, V, do, dos, dims, *a):
         (o, os_, lse), _ = ow.attn_prefill_window(q, qs, K, V, dims, window, sinks)
-        return ow.attn_prefill_window_bwd(q, qs, K, V, window, sinks, o, os_, lse, do, dos, dims)[0]
+        return ow.attn_prefill_window_bwd(q, qs, K, V, window, sinks, lse, do, dos, dims)[0]
     stack = mock.patch.multiple(ob, attn_prefill=fwd, attn_prefill_bwd=bwd)
     stack2 = mock.patch.object(oo, "attn_prefill", fwd)
     return stack, stack2

@@ -64,7 +64,7 @@ def test_backward_matches_autograd(window, sinks):
     do = gi.normal_bf16(3, "do", q.shape)
     dos = gi.normal_bf16(3, "dosh", qs.shape)
     (o, os_, lse), _ = ow.attn_prefill_window(q, qs, K, V, dims, window, sinks)
-    (dq, dqs, dK, dV), _ = ow.attn_prefill_window_bwd(q, qs, K, V, window, sinks, o, os_, lse, do, dos, dims)
+    (dq, dqs, dK, dV), _ = ow.attn_prefill_window_bwd(q, qs, K, V, window, sinks, lse, do, dos, dims)
     tq, tqs, tK, tV = (torch.tensor(orc.f64(x), requires_grad=True) for x in (q, qs, K, V))
     t = torch.arange(17)
     hide = t[None] > t[:, None]
@@ -87,7 +87,7 @@ def test_backward_matches_finite_differences():
     vis = ow.sees(np.arange(15)[:, None], np.arange(15)[None], 4, 2)
     f = lambda a, b, c: float((ow.masked_attention(a, vis, b, c, 0.125)[0] * dO).sum())
     o, lse = ow.masked_attention(q, vis, K, V, 0.125)
-    grads, _ = ow.masked_attention_bwd(q, vis, K, V, dO, 0.125, o, lse)
+    grads, _ = ow.masked_attention_bwd(q, vis, K, V, dO, 0.125, lse)
     h = 1e-5
     for i, g in enumerate(grads):
         u = rng.standard_normal((15, 64))
