@@ -80,7 +80,7 @@ struct AttnBwdParams {
   const gqe_bf16_t* q_sh;
   const gqe_bf16_t* K;
   const gqe_bf16_t* V;
-  float* part;                      // cut walks' sums: [2 * CTAs, 2 (dK, dV), 128, d] fp32
+  float* part;                      // cut walks' sums: [2 * stretches, 2 (dK, dV), 128, d] fp32
 };
 
 struct AttnBwdLayout {
@@ -90,13 +90,16 @@ struct AttnBwdLayout {
 };
 
 
-// Windowed backward (attn_bwd_window.cu): where each CTA starts in the list of
-// (sequence, key tile, query tile of its walk), cut into equal stretches.
-constexpr int kBwdWindowCtas = 148;
+// Windowed backward (attn_bwd_window.cu): the list of (sequence, key tile, query
+// tile of its walk) cut into n_rounds * n_ctas equal stretches; CTA c runs
+// stretches c, n_ctas + c, 2 n_ctas + c, ...
+constexpr int kBwdWindowCtas = 148, kBwdWindowRounds = 4;
 struct AttnBwdSchedule {
-  int n_ctas;
-  int seq[kBwdWindowCtas + 1], jt[kBwdWindowCtas + 1], off[kBwdWindowCtas + 1];
-  int count[kBwdWindowCtas];        // query tiles of each CTA
+  int n_ctas, n_rounds;
+  int seq[kBwdWindowCtas * kBwdWindowRounds];      // where each stretch starts
+  int jt[kBwdWindowCtas * kBwdWindowRounds];
+  int off[kBwdWindowCtas * kBwdWindowRounds];
+  int count[kBwdWindowCtas * kBwdWindowRounds];    // its query tiles
 };
 // The schedule, the bytes of scratch (attn_bwd_layout's, then the cut walks'
 // sums) and where the sums lie.

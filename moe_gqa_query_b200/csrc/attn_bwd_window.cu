@@ -12,13 +12,14 @@
 // per key tile, as without a window, then spends a third of its time starting
 // and ending (5.5 of 16.6 us at a window of 512, d = 64) and waits for the sink
 // tiles.  Here the walks of all key tiles of all sequences form one list of
-// (key tile, query tile) pairs, cut into equal stretches, one per SM, and each
-// CTA runs its stretch as one pipeline: the loads and products of the next key
-// tile start while the last one's are still running.  A walk cut by a stretch's
-// end leaves its dK, dV sums in fp32 in a slot of its CTA, and
+// (key tile, query tile) pairs, cut into equal stretches, one or a few per SM,
+// and each CTA runs its stretches as one pipeline: the loads and products of the
+// next key tile start while the last one's are still running.  A walk cut by a
+// stretch's end leaves its dK, dV sums in fp32 in a slot of the stretch, and
 // attn_bwd_window_post_kernel adds the slots of a walk in their order, so dK
 // and dV do not depend on timing.  dQ goes through TMA reduce-add into fp32 as
-// in attn_bwd.cu.
+// in attn_bwd.cu; with several stretches per CTA all CTAs work on one part of
+// the sequences at a time, so that the part's dQ sums stay in L2 (attn_bwd_window_plan).
 //
 // CTA: 512 threads, roles, tensor memory and barriers as in attn_bwd.cu, with
 // every ring counted over the whole stretch, but for d = 128: dK reads dS from
@@ -31,10 +32,11 @@
 //
 // Delta = dO . O takes the forward's O, which is rounded to bf16.  The error is
 // |dO||O| 2^-9 a row, next to |dO||V - O| in dP - Delta: of no account when O
-// averages many keys, but as large as all other roundings together for a row
-// that sees two or three (dq of 3-token sequences 0.0039 off, norm-wise, against
-// 0.0018 in fp32).  Rows that see at most kFewKeys keys take Delta = sum_j P_j
-// dP_j in fp32 instead, in the prep kernel.
+// averages many keys (|O| is then about |V| / sqrt(n)), but as large as all other
+// roundings together for a row that sees two or three (dq of 3-token sequences
+// 0.0039 off, norm-wise, against 0.0018 in fp32).  Rows that see at most kFewKeys
+// keys take Delta = sum_j P_j dP_j in fp32 instead, in the prep kernel; at nine
+// keys what is left is a third of the other roundings, a tenth of their variance.
 //
 // P and dS are computed with packed pairs (f32x2): the prep kernel stores -LSE2
 // and -Delta, so a pair costs one FMA before its exponentials and one add and
@@ -49,7 +51,7 @@ namespace gqe {
 namespace {
 
 constexpr int kThreadsW = 512;
-constexpr int kFewKeys = 16;
+constexpr int kFewKeys = 8;
 constexpr int kTileW = 128;
 constexpr int kBoxW = 128 * 64 * 2;   // one 128-row x 64-column bf16 TMA box
 
@@ -110,6 +112,7 @@ struct Stretch {
   int n_r, total;    // routed query tiles and all query tiles of the whole walk
   int cnt, n;        // query tiles of the piece, position in it
   int item;          // pieces before this one
+  int id;            // the stretch
 
   __device__ __forceinline__ void open(const AttnBwdParams& p) {
     int n_s;
@@ -118,21 +121,31 @@ struct Stretch {
     cnt = min(total - off, left);
     n = 0;
   }
-  __device__ __forceinline__ void start(const AttnBwdParams& p, const AttnBwdSchedule& S) {
-    left = S.count[blockIdx.x];
-    s = S.seq[blockIdx.x];
+  __device__ __forceinline__ void load(const AttnBwdParams& p, const AttnBwdSchedule& S) {
+    left = S.count[id];
+    s = S.seq[id];
     b = s / p.G;
     g = s - b * p.G;
-    jt = S.jt[blockIdx.x];
-    off = S.off[blockIdx.x];
-    item = 0;
+    jt = S.jt[id];
+    off = S.off[id];
     open(p);
   }
-  __device__ __forceinline__ bool next_item(const AttnBwdParams& p) {
+  __device__ __forceinline__ void start(const AttnBwdParams& p, const AttnBwdSchedule& S) {
+    id = blockIdx.x;
+    item = 0;
+    load(p, S);
+  }
+  __device__ __forceinline__ bool next(const AttnBwdParams& p, const AttnBwdSchedule& S) {
+    if (++n < cnt) return true;
     left -= cnt;
-    if (left <= 0) return false;
-    off = 0;
     ++item;
+    if (left <= 0) {
+      id += S.n_ctas;
+      if (id >= S.n_ctas * S.n_rounds) return false;
+      load(p, S);
+      return true;
+    }
+    off = 0;
     if (++jt * kTileW >= p.T) {
       jt = 0;
       ++s;
@@ -140,10 +153,6 @@ struct Stretch {
     }
     open(p);
     return true;
-  }
-  __device__ __forceinline__ bool next(const AttnBwdParams& p) {
-    if (++n < cnt) return true;
-    return next_item(p);
   }
   __device__ __forceinline__ bool first() const { return n == 0; }
   __device__ __forceinline__ bool last() const { return n == cnt - 1; }
@@ -198,15 +207,15 @@ __device__ __forceinline__ void product_mm(uint32_t acc, uint32_t a, uint32_t b,
 }
 
 // One row of a key tile's dK and dV out of tensor memory, then acc_free.  A cut
-// walk's go to its slot in fp32 (slot 0 of the CTA when the piece starts inside
-// the walk, else slot 1), a whole walk's are rounded.
+// walk's go to its slot in fp32 (slot 0 of the stretch when the piece starts
+// inside the walk, else slot 1), a whole walk's are rounded.
 template <int D>
 __device__ __forceinline__ void read_acc(const Stretch& c, const AttnBwdParams& p, uint32_t tmem_lane, int kv,
                                          uint64_t* acc_free) {
   using C = BwdWinCfg<D>;
   const int kv_pos = c.jt * kTileW + kv;
   const bool whole = c.whole();
-  float* slot = p.part + ((size_t)(2 * blockIdx.x + (c.off > 0 ? 0 : 1)) * 2 * kTileW + kv) * D;
+  float* slot = p.part + ((size_t)(2 * c.id + (c.off > 0 ? 0 : 1)) * 2 * kTileW + kv) * D;
   const size_t orow = ((size_t)c.s * p.T + kv_pos) * D;
 #pragma unroll 1
   for (int c0 = 0; c0 < 2 * D; c0 += 32) {       // dK's columns, then dV's
@@ -344,7 +353,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
             tma_load_3d(smem + C::OffDO + so * C::TileBytes + bx * kBoxW, mo, &bar->o_full[so], bx * 64, row, seq);
         }
         ++N;
-      } while (c.next(p));
+      } while (c.next(p, sched));
     } else if (warp == 1) {
       // ---------------- MMA issuer A: S^T, dP^T, dV
       constexpr uint32_t idesc_s = idesc_bf16_f32(kTileW, kTileW, false, false);
@@ -405,7 +414,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
           if (nx.last()) umma_commit(&bar->v_empty[b]);
         }
         c = nx;
-        more = nx.next(p);
+        more = nx.next(p, sched);
       }
     } else if (warp == 2) {
       // ---------------- MMA issuer B: dK += dS^T Q_i, dQ_i = dS K_j
@@ -450,7 +459,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         }
         if (leader && c.last()) umma_commit(&bar->k_empty[b]);
         ++N;
-      } while (c.next(p));
+      } while (c.next(p, sched));
     }
   } else if (warp < 12) {
     set_regs_up<C::kWide ? 136 : 144>();
@@ -570,7 +579,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
       mbar_arrive(&bar->ds_full);
       mbar_arrive(&bar->q_empty[st]);
       ++N;
-    } while (c.next(p));
+    } while (c.next(p, sched));
   } else {
     if (C::kWide) set_regs_up<160>();
     // ---------------- dQ drain (TMA reduce-add into fp32); dK, dV at the end of each key tile
@@ -624,7 +633,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         }
       }
       ++N;
-    } while (c.next(p));
+    } while (c.next(p, sched));
   out:
     if (lane == 0) bulk_wait<0>();
   }
@@ -646,14 +655,73 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
   return d;
 }
 
+// The tokens of a sequence that see at most kFewKeys keys: the first ones, since
+// token t sees min(t + 1, ...) of them and never fewer than token t - 1.
+__host__ __device__ __forceinline__ int few_key_tokens(int T, int window, int sinks) {
+  return T <= kFewKeys || (long long)window + sinks <= kFewKeys ? T : kFewKeys;
+}
+
+// Delta of a row that sees at most kFewKeys keys, sum_j P_j dP_j, by one warp:
+// d/8 lanes a key, the loads of 64 / (d/8) keys in flight.  No shared memory: a
+// kernel that has 32 bytes of it makes the SMs set their L1 split anew between
+// the attention kernels around it, 8 us of a 42 us step.
+__device__ __forceinline__ void few_keys_delta(const AttnBwdParams& p, int n_few, int tokens) {
+  const int tpr = p.d / 8, lane = threadIdx.x & 31, part = lane % tpr, at_once = 32 / tpr;
+  int q = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (q >= n_few) return;
+  const int BG = p.B * p.G;
+  const bool shared = q >= BG * tokens * p.k;
+  if (shared) q -= BG * tokens * p.k;
+  const int kk = shared ? 1 : p.k;
+  const int sq = q / (tokens * kk), r = q - sq * tokens * kk;
+  const int t = r / kk, lo = max(0, t - p.window + 1), first = min(p.sinks, lo), n = first + t - lo + 1;
+  const long long src = (long long)sq * p.T * kk + r;
+  const long long kv0 = (long long)(shared ? sq * p.G + p.sg : sq) * p.T * tpr + part;
+  const uint4 qv = reinterpret_cast<const uint4*>((shared ? p.q_sh : p.q_routed) + src * p.d)[part];
+  const uint4 dov = reinterpret_cast<const uint4*>((shared ? p.do_sh : p.do_routed) + src * p.d)[part];
+  const float lse2 = p.lse[shared ? (long long)BG * p.T * p.k + src : src] * 1.4426950408889634f;
+  float delta = 0.f;
+  for (int j0 = lane / tpr; j0 < kFewKeys; j0 += 2 * at_once) {
+    float s[2], dp[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = min(j0 + i * at_once, n - 1);
+      const long long at = kv0 + (long long)(j < first ? j : lo + j - first) * tpr;
+      s[i] = dot8(qv, reinterpret_cast<const uint4*>(p.K)[at]);
+      dp[i] = dot8(dov, reinterpret_cast<const uint4*>(p.V)[at]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      for (int off = tpr >> 1; off > 0; off >>= 1) {
+        s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], off);
+        dp[i] += __shfl_xor_sync(0xFFFFFFFFu, dp[i], off);
+      }
+      if (j0 + i * at_once < n) delta = fmaf(ex2(fmaf(s[i], p.scale_log2, -lse2)), dp[i], delta);
+    }
+  }
+  for (int off = tpr; off < 32; off <<= 1) delta += __shfl_xor_sync(0xFFFFFFFFu, delta, off);
+  if (lane == 0)
+    p.delta[(shared ? (long long)BG * p.rows_pad : 0) + (long long)sq * (shared ? p.rows_pad_sh : p.rows_pad) + r] =
+        -delta;
+}
+
 // -Delta and -LSE2 of every row of the padded row space (LSE2 +inf and Delta 0
 // on padding rows, so their P is 0), and the dQ accumulator zeroed.  d/8 threads
-// a row, 16 bytes each; HBM-bound (o, dO, the accumulator).
-__global__ void __launch_bounds__(256) attn_bwd_window_prep_kernel(const __grid_constant__ AttnBwdParams p) {
+// a row, 16 bytes each; HBM-bound (o, dO, the accumulator).  The first
+// few_blocks blocks are few_keys_delta's instead: in the rows' own threads, one
+// key after the other, it was 12 us of a 160 us step, by its latency and by the
+// registers that took the other rows' occupancy (six blocks an SM, 40 registers
+// and a few spills in few_keys_delta, against 51 registers: 2 % of that step).
+__global__ void __launch_bounds__(256, 6) attn_bwd_window_prep_kernel(const __grid_constant__ AttnBwdParams p,
+                                                                   int few_blocks, int few_tokens) {
   pdl_launch_dependents();
   pdl_wait();
+  if ((int)blockIdx.x < few_blocks) {
+    few_keys_delta(p, p.B * few_tokens * (p.G * p.k + p.n_shared), few_tokens);
+    return;
+  }
   const int tpr = p.d / 8;
-  const long long gt = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long gt = (long long)(blockIdx.x - few_blocks) * 256 + threadIdx.x;
   const long long pr = gt / tpr;
   const int part = (int)(gt % tpr);
   if (pr >= p.n_rows_pad) return;      // whole rows: tpr divides 32
@@ -671,37 +739,21 @@ __global__ void __launch_bounds__(256) attn_bwd_window_prep_kernel(const __grid_
   float lse2 = INFINITY, delta = 0.f;
   if (valid) {
     lse2 = p.lse[shared ? (long long)BG * p.T * p.k + src : src] * 1.4426950408889634f;
-    const uint4 dov = reinterpret_cast<const uint4*>(dO)[part];
-    const int t = r / kk, lo = max(0, t - p.window + 1), first = min(p.sinks, lo), n = first + t - lo + 1;
-    if (n <= kFewKeys) {
-      const uint4 qv = reinterpret_cast<const uint4*>((shared ? p.q_sh : p.q_routed) + src * p.d)[part];
-      const size_t kv0 = (size_t)(shared ? sq * p.G + p.sg : sq) * p.T * tpr + part;
-      for (int j = 0; j < n; ++j) {
-        const size_t at = kv0 + (size_t)(j < first ? j : lo + j - first) * tpr;
-        float s = dot8(qv, reinterpret_cast<const uint4*>(p.K)[at]);
-        float dp = dot8(dov, reinterpret_cast<const uint4*>(p.V)[at]);
-        for (int off = tpr >> 1; off > 0; off >>= 1) {
-          s += __shfl_xor_sync(row_lanes, s, off);
-          dp += __shfl_xor_sync(row_lanes, dp, off);
-        }
-        delta = fmaf(ex2(fmaf(s, p.scale_log2, -lse2)), dp, delta);
-      }
-    } else {
-      delta = dot8(reinterpret_cast<const uint4*>(o)[part], dov);
-      for (int off = tpr >> 1; off > 0; off >>= 1) delta += __shfl_xor_sync(row_lanes, delta, off);
-    }
+    delta = dot8(reinterpret_cast<const uint4*>(o)[part], reinterpret_cast<const uint4*>(dO)[part]);
+    for (int off = tpr >> 1; off > 0; off >>= 1) delta += __shfl_xor_sync(row_lanes, delta, off);
   }
   float4* acc = reinterpret_cast<float4*>(p.dq_acc + pr * p.d + part * 8);
   acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
   acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (part == 0) {
-    p.delta[pr] = -delta;
+    if (!valid || r >= few_tokens * kk) p.delta[pr] = -delta;
     p.lse2[pr] = -lse2;
   }
 }
 
 // dK, dV of a walk that the stretches' ends cut: the pieces of the walk cut
-// between CTAs c-1 and c added in their order, when that is the walk's first cut.
+// between stretches c-1 and c added in their order, when that is the walk's
+// first cut.
 // Each of the kJoinBlocks blocks takes its part of the tile.
 constexpr int kJoinBlocks = 8;
 __device__ __forceinline__ void join_walk(const AttnBwdParams& p, const AttnBwdSchedule& S, int c, int block) {
@@ -709,7 +761,7 @@ __device__ __forceinline__ void join_walk(const AttnBwdParams& p, const AttnBwdS
   if (S.off[c] == 0) return;                                                     // the walk starts here
   if (S.seq[c - 1] == s && S.jt[c - 1] == jt && S.off[c - 1] > 0) return;         // cut before
   int last = c;
-  while (last + 1 < S.n_ctas && S.seq[last + 1] == s && S.jt[last + 1] == jt && S.off[last + 1] > 0) ++last;
+  while (last + 1 < S.n_ctas * S.n_rounds && S.seq[last + 1] == s && S.jt[last + 1] == jt && S.off[last + 1] > 0) ++last;
   const size_t slot = (size_t)2 * kTileW * p.d;
   const int per = p.d / 4;
   for (int e = block * 256 + threadIdx.x; e < 2 * kTileW * per; e += kJoinBlocks * 256) {
@@ -729,13 +781,13 @@ __device__ __forceinline__ void join_walk(const AttnBwdParams& p, const AttnBwdS
   }
 }
 
-// The first (n_ctas - 1) * kJoinBlocks blocks join the cut walks, the others
+// The first (stretches - 1) * kJoinBlocks blocks join the cut walks, the others
 // round dq from its fp32 sums (d/8 threads a row, valid rows only).
 __global__ void __launch_bounds__(256)
 attn_bwd_window_post_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ AttnBwdSchedule S) {
   pdl_launch_dependents();
   pdl_wait();
-  const int n_join = (S.n_ctas - 1) * kJoinBlocks;
+  const int n_join = (S.n_ctas * S.n_rounds - 1) * kJoinBlocks;
   if ((int)blockIdx.x < n_join) {
     join_walk(p, S, blockIdx.x / kJoinBlocks + 1, blockIdx.x % kJoinBlocks);
     return;
@@ -766,7 +818,14 @@ attn_bwd_window_post_kernel(const __grid_constant__ AttnBwdParams p, const __gri
 }  // namespace
 
 // Walks in the order of the sequences, and of the key tiles in each, cut into
-// stretches of equal length (to within one query tile).
+// stretches of equal length (to within one query tile).  One round of stretches
+// unless dQ's fp32 sums would not stay in L2: every query tile is added to about
+// window / 128 + 2 times, from DRAM if all sequences are worked on at once (2 x
+// 8192 tokens, 17 heads of d = 128, 143 MB of sums: 3.3 GB of DRAM traffic in one
+// round), so rounds of at most 64 MB of sums, while a stretch keeps 16 query
+// tiles (a cut costs two fp32 tiles written and read).
+constexpr long long kRoundBytes = 64 << 20;
+
 void attn_bwd_window_plan(int B, int T, int G, int k, int n_shared, int sg, int d, int window, int sinks,
                           AttnBwdSchedule* S, size_t* off_part, size_t* bytes) {
   const int n_jt = (T + kTileW - 1) / kTileW;
@@ -778,8 +837,15 @@ void attn_bwd_window_plan(int B, int T, int G, int k, int n_shared, int sg, int 
     extra += s;
   }
   const long long per_b = plain * G + extra, total = per_b * B;
-  const int n = total < kBwdWindowCtas ? (int)total : kBwdWindowCtas;
-  S->n_ctas = n;
+  AttnBwdLayout L;
+  attn_bwd_layout(B, T, G, k, n_shared, d, &L);
+  const int ctas = total < kBwdWindowCtas ? (int)total : kBwdWindowCtas;
+  int rounds = (int)((L.n_rows_pad * d * 4 + kRoundBytes - 1) / kRoundBytes);
+  if (rounds > kBwdWindowRounds) rounds = kBwdWindowRounds;
+  while (rounds > 1 && total / ((long long)ctas * rounds) < 16) --rounds;
+  const int n = ctas * rounds;
+  S->n_ctas = ctas;
+  S->n_rounds = rounds;
   int seq = -1, j = 0;
   long long before = 0;                // query tiles before walk (seq, j)
   for (int c = 0; c < n; ++c) {
@@ -806,8 +872,6 @@ void attn_bwd_window_plan(int B, int T, int G, int k, int n_shared, int sg, int 
     S->jt[c] = j;
     S->off[c] = (int)(at - before);
   }
-  AttnBwdLayout L;
-  attn_bwd_layout(B, T, G, k, n_shared, d, &L);
   *off_part = (L.bytes + 255) & ~size_t(255);
   *bytes = *off_part + (size_t)2 * n * 2 * kTileW * d * sizeof(float);
 }
@@ -829,12 +893,17 @@ cudaError_t launch_attn_bwd_window(const CUtensorMap& mQ, const CUtensorMap& mQs
                                    const CUtensorMap& mdQ, const AttnBwdParams& p, const AttnBwdSchedule& S,
                                    cudaStream_t stream) {
   const long long row_blocks = (p.n_rows_pad * (p.d / 8) + 255) / 256;
-  cudaError_t e = launch_kernel(attn_bwd_window_prep_kernel, dim3((unsigned)row_blocks), dim3(256), 0, stream, 1, p);
+  const int few_tokens = few_key_tokens(p.T, p.window, p.sinks);
+  const int few_blocks = (p.B * few_tokens * (p.G * p.k + p.n_shared) + 7) / 8;
+  cudaError_t e = launch_kernel(attn_bwd_window_prep_kernel, dim3((unsigned)(row_blocks + few_blocks)), dim3(256), 0,
+                                stream, 1, p, few_blocks, few_tokens);
   if (e != cudaSuccess) return e;
   e = p.d == 64 ? launch_win<64>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S, stream)
                 : launch_win<128>(mQ, mQs, mdO, mdOs, mK, mV, mdQ, p, S, stream);
   if (e != cudaSuccess) return e;
-  return launch_kernel(attn_bwd_window_post_kernel, dim3((unsigned)(row_blocks + (S.n_ctas - 1) * kJoinBlocks)), dim3(256), 0, stream, 1, p, S);
+  return launch_kernel(attn_bwd_window_post_kernel,
+                       dim3((unsigned)(row_blocks + (S.n_ctas * S.n_rounds - 1) * kJoinBlocks)), dim3(256), 0, stream,
+                       1, p, S);
 }
 
 }  // namespace gqe

@@ -79,7 +79,7 @@ def masked_attention_error_bound(q, vis, K, V, scale):
     return out
 
 
-FEW_KEYS = 16       # rows that see at most this many keys have their Delta from P and dP (see below)
+FEW_KEYS = 8        # rows that see at most this many keys have their Delta from P and dP (see below)
 
 
 def masked_attention_bwd(q, vis, K, V, dO, scale, lse):

@@ -84,10 +84,10 @@ def test_workspace_sizes():
     d = dims()
     plain = gq.gqe_workspace_size(d, gq.GQE_OP_ATTN_BWD)
     size = lambda *a: gq.gqe_window_workspace_size(*a)  # noqa: E731
-    # two fp32 [2, 128, d] slots for each stretch of the walks, one stretch per SM at most
+    # two fp32 [2, 128, d] slots for each stretch of the walks, four stretches per SM at most
     for window in (0, 1, 64, 300, 10 ** 9):
         w = size(d, gq.GQE_OP_ATTN_WINDOW_BWD, 0, window, 5)
-        assert plain < w <= plain + 255 + 148 * 2 * 2 * 128 * 64 * 4
+        assert plain < w <= plain + 255 + 4 * 148 * 2 * 2 * 128 * 64 * 4
     assert size(dims(T=1), gq.GQE_OP_ATTN_DECODE_WINDOW, 4096, 100, 4) == 0
     assert size(dims(T=128), gq.GQE_OP_ATTN_TREE, 4096, 0, 0) == 0
     for args, status in (((d, gq.GQE_OP_ATTN_TREE, 4096, 0, 0), 2), ((dims(T=8), gq.GQE_OP_ATTN_TREE, 0, 0, 0), 1),
