@@ -197,11 +197,14 @@ gqe_status gqe_attn_prefill_window(const gqe_dims* dims, const gqe_bf16* q_route
 /* Backward of gqe_attn_prefill_window for the same window and sinks; the other
  * arguments are those of gqe_attn_prefill_bwd (o and lse from
  * gqe_attn_prefill_window).  Delta is taken from P and dP in fp32, not from O
- * (which is rounded), for rows that see at most 16 keys.  dK and dV do not
+ * (which is rounded), for rows that see at most 8 keys.  dK and dV do not
  * depend on timing; dq is summed over key tiles in an order that may differ
  * between runs.
  *   ws: gqe_window_workspace_size(GQE_OP_ATTN_WINDOW_BWD) bytes, 256-byte
- *   aligned. */
+ *   aligned.
+ * Errors: GQE_ERR_UNSUPPORTED for 2^31 rows or more, each sequence's rows of a
+ * group counted in tiles of 128 (its scratch would be 137 GB), else as
+ * gqe_attn_prefill_bwd. */
 gqe_status gqe_attn_prefill_window_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
                                        const gqe_bf16* K, const gqe_bf16* V, int window, int sinks,
                                        const gqe_bf16* o_routed, const gqe_bf16* o_sh, const float* lse,

@@ -322,15 +322,15 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
           if (leader) {
             mbar_arrive_expect_tx(&bar->k_full[b], C::TileBytes);
             for (int bx = 0; bx < C::NB; ++bx)
-              tma_load_3d(smem + C::OffK + b * C::TileBytes + bx * kBoxW, &mapK, &bar->k_full[b], bx * 64, c.jt * kTileW,
-                          c.s);
+              tma_load_3d(smem + C::OffK + b * C::TileBytes + bx * kBoxW, &mapK, &bar->k_full[b], bx * 64,
+                          c.jt * kTileW, c.s);
           }
           if (c.item >= C::KVB && !wait_w(&bar->v_empty[b], ph)) break;
           if (leader) {
             mbar_arrive_expect_tx(&bar->v_full[b], C::TileBytes);
             for (int bx = 0; bx < C::NB; ++bx)
-              tma_load_3d(smem + C::OffV + b * C::TileBytes + bx * kBoxW, &mapV, &bar->v_full[b], bx * 64, c.jt * kTileW,
-                          c.s);
+              tma_load_3d(smem + C::OffV + b * C::TileBytes + bx * kBoxW, &mapV, &bar->v_full[b], bx * 64,
+                          c.jt * kTileW, c.s);
           }
         }
         const int st = N & 1, so = N % C::OST;
@@ -761,7 +761,8 @@ __device__ __forceinline__ void join_walk(const AttnBwdParams& p, const AttnBwdS
   if (S.off[c] == 0) return;                                                     // the walk starts here
   if (S.seq[c - 1] == s && S.jt[c - 1] == jt && S.off[c - 1] > 0) return;         // cut before
   int last = c;
-  while (last + 1 < S.n_ctas * S.n_rounds && S.seq[last + 1] == s && S.jt[last + 1] == jt && S.off[last + 1] > 0) ++last;
+  const int n = S.n_ctas * S.n_rounds;
+  while (last + 1 < n && S.seq[last + 1] == s && S.jt[last + 1] == jt && S.off[last + 1] > 0) ++last;
   const size_t slot = (size_t)2 * kTileW * p.d;
   const int per = p.d / 4;
   for (int e = block * 256 + threadIdx.x; e < 2 * kTileW * per; e += kJoinBlocks * 256) {

@@ -71,7 +71,8 @@ struct __align__(16) CacheShared {
 
 template <int D>
 constexpr size_t cache_smem() {
-  return 1024 + CacheCfg<D>::QBytes + (CacheCfg<D>::KST + CacheCfg<D>::VST) * CacheCfg<D>::KVBytes + sizeof(CacheShared);
+  using C = CacheCfg<D>;
+  return 1024 + C::QBytes + (C::KST + C::VST) * C::KVBytes + sizeof(CacheShared);
 }
 
 // One sequence's keys as this query tile's list of key tiles.
@@ -113,7 +114,7 @@ struct RowState {
 template <int D, int NC>
 __device__ __forceinline__ RowState cache_softmax(const CacheAttnParams& p, const CacheList& cl, CacheShared* sh,
                                                   uint8_t* sV, uint32_t lane_base, int first, int n, int col0,
-                                                  int t_r, const uint32_t* anc, int depth) {
+                                                  const uint32_t* anc, int depth) {
   using C = CacheCfg<D>;
   constexpr int KT = C::KT;
   volatile int* abort = &sh->abort;
@@ -464,7 +465,8 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
         const int e = tid + i * kCacheThreads, c = e % (D / 8);
         if (e / (D / 8) < lanes_rep)
           for (int L = e / (D / 8); L < kRowsQ; L += lanes_rep)
-            st_shared_v4(sQ + (c >> 3) * C::QBox + L * 128 + (((c & 7) ^ (L & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+            st_shared_v4(sQ + (c >> 3) * C::QBox + L * 128 + (((c & 7) ^ (L & 7)) << 4), v[i].x, v[i].y, v[i].z,
+                         v[i].w);
       }
     }
     fence_proxy_async_smem();
@@ -528,11 +530,11 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
       const uint32_t* anc = reinterpret_cast<const uint32_t*>(&sh->anc[cur][live ? t_r : 0]);
       RowState st;
       if (rep == 4)
-        st = cache_softmax<D, KT / 4>(p, cl, sh, sV, lane_base, first, n, q * (KT / 4), t_r, anc, depth);
+        st = cache_softmax<D, KT / 4>(p, cl, sh, sV, lane_base, first, n, q * (KT / 4), anc, depth);
       else if (rep == 2)
-        st = cache_softmax<D, KT / 2>(p, cl, sh, sV, lane_base, first, n, q * (KT / 2), t_r, anc, depth);
+        st = cache_softmax<D, KT / 2>(p, cl, sh, sV, lane_base, first, n, q * (KT / 2), anc, depth);
       else
-        st = cache_softmax<D, KT>(p, cl, sh, sV, lane_base, first, n, 0, t_r, anc, depth);
+        st = cache_softmax<D, KT>(p, cl, sh, sV, lane_base, first, n, 0, anc, depth);
       // ---------------- epilogue: join the repeats through shared memory (the
       // operand tiles are no longer read)
       float* sO = reinterpret_cast<float*>(smem);
@@ -660,8 +662,8 @@ static cudaError_t launch_cache(const CUtensorMap& mK, const CUtensorMap& mV, co
   auto kern = attn_cache_kernel<D>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kern), cache_smem<D>(), p.n_split > 8);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)items), dim3(kCacheThreads), cache_smem<D>(), stream, p.n_split, mK, mV, mKt,
-                       mVt, p);
+  return launch_kernel(kern, dim3((unsigned)items), dim3(kCacheThreads), cache_smem<D>(), stream, p.n_split, mK, mV,
+                       mKt, mVt, p);
 }
 
 cudaError_t launch_attn_cache(const CUtensorMap& mK, const CUtensorMap& mV, const CUtensorMap& mKt,

@@ -40,6 +40,7 @@ constexpr int kRowsPW = 128;          // query rows per tile
 constexpr int kThreadsPW = 192;
 constexpr int kNarrow = 32;           // keys of a narrow sink tile
 constexpr float kRescalePW = 8.0f;
+
 struct __align__(8) PrefillWinBarriers {
   uint64_t q_full;
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
@@ -252,7 +253,6 @@ attn_prefill_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
 
   if (warp == 4) {
     // ---------------- MMA issuer
-
     constexpr uint32_t idesc_s = idesc_bf16_f32(kRowsPW, KT, false, false);
     constexpr uint32_t idesc_n = idesc_bf16_f32(kRowsPW, kNarrow, false, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(kRowsPW, D, false, true);
@@ -298,7 +298,6 @@ attn_prefill_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
     }
   } else if (warp == 5) {
     // ---------------- producer: the K and V tiles past the first ST
-
     for (int j = ST; j < kl.n; ++j) {
       const int s = j % ST;
       if (!mbar_wait_warp(&bar->k_empty[s], (j / ST - 1) & 1, abort)) break;
@@ -340,7 +339,8 @@ attn_prefill_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
           uint32_t pk[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            pk[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv_l, __uint_as_float(o[8 * c + 2 * e + 1]) * inv_l);
+            pk[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv_l,
+                                __uint_as_float(o[8 * c + 2 * e + 1]) * inv_l);
           d4[c] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
       }

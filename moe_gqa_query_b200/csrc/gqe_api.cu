@@ -496,6 +496,8 @@ static gqe_status prefill_bwd_common(const gqe_dims* dims, const gqe_bf16* q_rou
   attn_bwd_layout(B, T, G, k, dims->n_shared, d, &L);
   if (!has_window(dims, window)) window = T;
   const int n_sinks = sinks < T ? sinks : T;
+  // the windowed kernels count rows of the padded row space in 32 bits
+  GQE_REQUIRE(!win || L.n_rows_pad <= 0x7FFFFFFFll, GQE_ERR_UNSUPPORTED);
   AttnBwdSchedule sched;
   size_t off_part = 0, need = L.bytes;
   if (win)
@@ -563,8 +565,8 @@ gqe_status gqe_attn_prefill_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, 
                                 const gqe_bf16* o_sh, const float* lse, const gqe_bf16* do_routed,
                                 const gqe_bf16* do_sh, gqe_bf16* dq_routed, gqe_bf16* dq_sh, gqe_bf16* dK,
                                 gqe_bf16* dV, void* ws, size_t ws_bytes, gqe_stream stream) {
-  return prefill_bwd_common(dims, q_routed, q_sh, K, V, false, 0, 0, o_routed, o_sh, lse, do_routed, do_sh, dq_routed, dq_sh,
-                            dK, dV, ws, ws_bytes, stream);
+  return prefill_bwd_common(dims, q_routed, q_sh, K, V, false, 0, 0, o_routed, o_sh, lse, do_routed, do_sh, dq_routed,
+                            dq_sh, dK, dV, ws, ws_bytes, stream);
 }
 
 gqe_status gqe_attn_prefill_window_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
@@ -683,6 +685,9 @@ gqe_status gqe_window_workspace_size(const gqe_dims* dims, int op, int L_max, in
   GQE_REQUIRE(bytes && window >= 0 && sinks >= 0, GQE_ERR_INVALID_ARG);
   const int B = dims->B, T = dims->T, G = dims->G, k = dims->k, d = dims->d_head;
   if (op == GQE_OP_ATTN_WINDOW_BWD) {
+    AttnBwdLayout L;
+    attn_bwd_layout(B, T, G, k, dims->n_shared, d, &L);
+    GQE_REQUIRE(L.n_rows_pad <= 0x7FFFFFFFll, GQE_ERR_UNSUPPORTED);
     AttnBwdSchedule sched;
     size_t off_part;
     attn_bwd_window_plan(B, T, G, k, dims->n_shared, dims->shared_kv_group, d, has_window(dims, window) ? window : T,
@@ -699,7 +704,6 @@ gqe_status gqe_window_workspace_size(const gqe_dims* dims, int op, int L_max, in
   }
   return GQE_ERR_INVALID_ARG;
 }
-
 
 gqe_status gqe_attn_decode(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh, const gqe_bf16* Kc,
                            const gqe_bf16* Vc, int L_max, const int32_t* cache_len, gqe_bf16* o_routed,

@@ -45,6 +45,15 @@ def test_prefill_window_bwd_arguments():
     assert call(64, 4, ok, 128, need) == 3        # not 256-byte aligned
 
 
+def test_prefill_window_bwd_row_count():
+    # one-token sequences take a 128-row tile each: 2^24 of them are 2^31 rows
+    size = lambda B: lib.gqe_window_workspace_size(  # noqa: E731
+        ctypes.byref(dims(B=B, T=1, G=1, E=4, k=1, D=64, n_shared=0)), gq.GQE_OP_ATTN_WINDOW_BWD, 0, 0, 0,
+        ctypes.byref(ctypes.c_size_t()))
+    assert size((1 << 24) - 1) == 0
+    assert size(1 << 24) == 2
+
+
 def tree(d, L=100, q=256, Kt=256, parent=256, Kc=256, clen=256, window=0, sinks=0, o=256):
     return lib.gqe_attn_tree(ctypes.byref(d), q, 256, Kt, 256, parent, None, Kc, 256, L, clen, window, sinks, o, 256, None,
                              0, None)
