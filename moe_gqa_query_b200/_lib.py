@@ -293,6 +293,15 @@ def _dev(t, name, dtype, dev, optional=False):
     return p
 
 
+def _lens(t, name, n, dev, optional=False):
+    """_dev of an int32 tensor of exactly n entries (lengths, parents, paths: a
+    narrower one would be read past its end)."""
+    p = _dev(t, name, _I32, dev, optional)
+    if p is not None and t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
+    return p
+
+
 def _scratch(ws, dev):
     """Pointer and size of a scratch tensor that may be absent."""
     return (None, 0) if ws is None else (_dev(ws, "ws", ws.dtype, dev), ws.numel() * ws.element_size())
@@ -302,8 +311,9 @@ def gqe_attn_prefill_window(dims, q_routed, q_sh, K, V, window, sinks, o_routed,
     dev = torch.cuda.current_device()
     _check("gqe_attn_prefill_window", lib.gqe_attn_prefill_window(
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
-        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), int(window), int(sinks), _dev(o_routed, "o_routed", _BF16, dev),
-        _dev(o_sh, "o_sh", _BF16, dev, True), _dev(lse, "lse", _F32, dev, True), _stream(stream, dev)))
+        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), int(window), int(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True),
+        _dev(lse, "lse", _F32, dev, True), _stream(stream, dev)))
 
 
 def gqe_attn_prefill_window_bwd(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, do_routed, do_sh,
@@ -312,8 +322,9 @@ def gqe_attn_prefill_window_bwd(dims, q_routed, q_sh, K, V, window, sinks, o_rou
     wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_prefill_window_bwd", lib.gqe_attn_prefill_window_bwd(
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
-        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), int(window), int(sinks), _dev(o_routed, "o_routed", _BF16, dev),
-        _dev(o_sh, "o_sh", _BF16, dev, True), _dev(lse, "lse", _F32, dev), _dev(do_routed, "do_routed", _BF16, dev),
+        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), int(window), int(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True),
+        _dev(lse, "lse", _F32, dev), _dev(do_routed, "do_routed", _BF16, dev),
         _dev(do_sh, "do_sh", _BF16, dev, True), _dev(dq_routed, "dq_routed", _BF16, dev),
         _dev(dq_sh, "dq_sh", _BF16, dev, True), _dev(dK, "dK", _BF16, dev), _dev(dV, "dV", _BF16, dev), wp, ws_bytes,
         _stream(stream, dev)))
@@ -326,8 +337,8 @@ def gqe_attn_decode_window(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, windo
     _check("gqe_attn_decode_window", lib.gqe_attn_decode_window(
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
         _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max),
-        _dev(cache_len, "cache_len", _I32, dev), int(window), int(sinks), _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes,
-        _stream(stream, dev)))
+        _lens(cache_len, "cache_len", dims.B, dev), int(window), int(sinks), _dev(o_routed, "o_routed", _BF16, dev),
+        _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes, _stream(stream, dev)))
 
 
 def gqe_attn_tree(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max, cache_len, window, sinks, o_routed,
@@ -338,10 +349,11 @@ def gqe_attn_tree(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max,
     wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_tree", lib.gqe_attn_tree(
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
-        _dev(Kt, "Kt", _BF16, dev), _dev(Vt, "Vt", _BF16, dev), _dev(parent, "parent", _I32, dev),
-        _dev(tree_len, "tree_len", _I32, dev, True), _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev),
-        int(L_max), _dev(cache_len, "cache_len", _I32, dev), int(window), int(sinks),
-        _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes, _stream(stream, dev)))
+        _dev(Kt, "Kt", _BF16, dev), _dev(Vt, "Vt", _BF16, dev), _lens(parent, "parent", dims.B * dims.T, dev),
+        _lens(tree_len, "tree_len", dims.B, dev, True), _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev),
+        int(L_max), _lens(cache_len, "cache_len", dims.B, dev), int(window), int(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes,
+        _stream(stream, dev)))
 
 
 def gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, L_max, cache_len, new_len, stream=None):
@@ -349,9 +361,10 @@ def gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, L_max, cache_len, new
     new_len (may be cache_len) = cache_len + n_accept."""
     dev = torch.cuda.current_device()
     _check("gqe_cache_commit", lib.gqe_cache_commit(
-        ctypes.byref(dims), _dev(Kt, "Kt", _BF16, dev), _dev(Vt, "Vt", _BF16, dev), _dev(path, "path", _I32, dev),
-        _dev(n_accept, "n_accept", _I32, dev), _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max),
-        _dev(cache_len, "cache_len", _I32, dev), _dev(new_len, "new_len", _I32, dev), _stream(stream, dev)))
+        ctypes.byref(dims), _dev(Kt, "Kt", _BF16, dev), _dev(Vt, "Vt", _BF16, dev),
+        _lens(path, "path", dims.B * dims.T, dev), _lens(n_accept, "n_accept", dims.B, dev), _dev(Kc, "Kc", _BF16, dev),
+        _dev(Vc, "Vc", _BF16, dev), int(L_max), _lens(cache_len, "cache_len", dims.B, dev),
+        _lens(new_len, "new_len", dims.B, dev), _stream(stream, dev)))
 
 
 def gqe_combine(dims, o_routed, o_sh, topk_w, h, stream=None):

@@ -435,6 +435,30 @@ def test_commit_out_of_range_is_flagged_and_contained():
 # ----------------------------------------------------------------------------
 # streams, graphs, workspaces
 
+def test_index_tensors_of_the_wrong_size_are_refused():
+    """Lengths, parents and paths of another size than the call reads raise
+    before anything is launched."""
+    B, G, T, L, d = 2, 1, 4, 32, 64
+    dims = gq.make_dims(D(B=B, T=T, G=G))
+    rows = torch.zeros(B, G, T, d, dtype=torch.bfloat16, device="cuda")
+    cache = torch.zeros(B, G, L, d, dtype=torch.bfloat16, device="cuda")
+    n = lambda *shape: torch.zeros(*shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    commit = lambda path=n(B, T), acc=n(B), ln=n(B), new=n(B): gq.gqe_cache_commit(  # noqa: E731
+        dims, rows, rows, path, acc, cache, cache, L, ln, new)
+    commit()
+    for bad in (dict(path=n(B, T - 1)), dict(acc=n(B - 1)), dict(ln=n(B + 1)), dict(new=n(1))):
+        with pytest.raises(ValueError, match="entries"):
+            commit(**bad)
+    o, os_ = torch.empty_like(rows), torch.empty(B, T, d, dtype=torch.bfloat16, device="cuda")
+    tree = lambda par=n(B, T) - 1, tl=None, ln=n(B): gq.gqe_attn_tree(  # noqa: E731
+        dims, rows, rows.view(B, T, d), rows, rows, par, tl, cache, cache, L, ln, 0, 0, o, os_)
+    tree()
+    for bad in (dict(par=n(B, T + 1)), dict(tl=n(1)), dict(ln=n(B, 2))):
+        with pytest.raises(ValueError, match="entries"):
+            tree(**bad)
+    assert gq.gqe_device_error() == 0
+
+
 def test_calls_run_on_the_stream_they_are_given():
     dims, L, lens, tlens, window, sinks, chain = TREE["window"]
     x = _cache_inputs(dims, L, 37)
