@@ -32,6 +32,11 @@
 // Keys no row sees (past the lengths, or between the sinks and the first
 // row's window) may hold anything: their scores are masked by selection and
 // their V rows are zeroed in shared memory before P V reads them.
+//
+// Bound by HBM where there are many keys: 64 sequences under a 4096-token window
+// (d = 64, 8 groups) 90 us, 0.92 of the measured copy bandwidth; 64 trees of 32
+// tokens over 32768-token caches 675 us, 0.99.  Few keys: by latency, start 3 us,
+// about 1 us a key tile, join 2-3 us (one tree of 8 tokens, 4096 rows: 10.3 us).
 #include "attn.cuh"
 #include "launch.cuh"
 
@@ -589,7 +594,9 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
 }
 
 // Accepted drafted rows to the end of the cache: one CTA per sequence, so that
-// new_len may be cache_len itself (the CTA has read it before it writes).
+// new_len may be cache_len itself (the CTA has read it before it writes).  Bound by
+// latency (lengths, path, row, one after the other): 2.6 us for one sequence, 4.6
+// us for 64 sequences of 17 rows of 8 groups, of which the bytes are 0.3 us.
 __global__ void __launch_bounds__(512) cache_commit_kernel(CommitParams p) {
   pdl_launch_dependents();
   pdl_wait();
