@@ -724,18 +724,16 @@ __global__ void __launch_bounds__(256, 6) attn_bwd_window_prep_kernel(const __gr
     few_keys_delta(p, p.B * few_tokens * (p.G * p.k + p.n_shared), few_tokens);
     return;
   }
-  const int tpr = p.d / 8;
-  const long long gt = (long long)(blockIdx.x - few_blocks) * 256 + threadIdx.x;
-  const long long pr = gt / tpr;
-  const int part = (int)(gt % tpr);
-  if (pr >= p.n_rows_pad) return;      // whole rows: tpr divides 32
+  const int log_tpr = p.d == 64 ? 3 : 4, tpr = 1 << log_tpr, part = threadIdx.x & (tpr - 1);
+  const int pr = (int)(blockIdx.x - few_blocks) * (256 >> log_tpr) + (threadIdx.x >> log_tpr);   // fewer than 2^31 rows
+  if (pr >= (int)p.n_rows_pad) return;      // whole rows: tpr divides 32
   const unsigned row_lanes = (tpr == 8 ? 0xFFu : 0xFFFFu) << (threadIdx.x & 31 & ~(tpr - 1));
   const int BG = p.B * p.G;
-  const long long routed_rows = (long long)BG * p.rows_pad;
+  const int routed_rows = BG * p.rows_pad;
   const bool shared = pr >= routed_rows;
-  const long long q2 = shared ? pr - routed_rows : pr;
+  const int q2 = shared ? pr - routed_rows : pr;
   const int pad = shared ? p.rows_pad_sh : p.rows_pad, kk = shared ? 1 : p.k;
-  const int sq = (int)(q2 / pad), r = (int)(q2 - (long long)sq * pad);       // sequence (or batch entry), row in it
+  const int sq = q2 / pad, r = q2 - sq * pad;       // sequence (or batch entry), row in it
   const bool valid = r < p.T * kk;
   const long long src = (long long)sq * p.T * kk + r;
   const gqe_bf16_t* o = (shared ? p.o_sh : p.o_routed) + src * p.d;
@@ -746,7 +744,7 @@ __global__ void __launch_bounds__(256, 6) attn_bwd_window_prep_kernel(const __gr
     delta = dot8(reinterpret_cast<const uint4*>(o)[part], reinterpret_cast<const uint4*>(dO)[part]);
     for (int off = tpr >> 1; off > 0; off >>= 1) delta += __shfl_xor_sync(row_lanes, delta, off);
   }
-  float4* acc = reinterpret_cast<float4*>(p.dq_acc + pr * p.d + part * 8);
+  float4* acc = reinterpret_cast<float4*>(p.dq_acc + (size_t)pr * p.d + part * 8);
   acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
   acc[1] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (part == 0) {
@@ -759,7 +757,7 @@ __global__ void __launch_bounds__(256, 6) attn_bwd_window_prep_kernel(const __gr
 // between stretches c-1 and c added in their order, when that is the walk's
 // first cut.
 // Each of the kJoinBlocks blocks takes its part of the tile.
-constexpr int kJoinBlocks = 8;
+constexpr int kJoinBlocks = 16;
 __device__ __forceinline__ void join_walk(const AttnBwdParams& p, const AttnBwdSchedule& S, int c, int block) {
   const int s = S.seq[c], jt = S.jt[c];
   if (S.off[c] == 0) return;                                                     // the walk starts here
@@ -797,23 +795,21 @@ attn_bwd_window_post_kernel(const __grid_constant__ AttnBwdParams p, const __gri
     join_walk(p, S, blockIdx.x / kJoinBlocks + 1, blockIdx.x % kJoinBlocks);
     return;
   }
-  const int tpr = p.d / 8;
-  const long long gt = (long long)(blockIdx.x - n_join) * 256 + threadIdx.x;
-  const long long pr = gt / tpr, routed_rows = (long long)p.B * p.G * p.rows_pad;
-  const int part = (int)(gt % tpr);
-  if (pr >= p.n_rows_pad) return;
+  const int log_tpr = p.d == 64 ? 3 : 4, part = threadIdx.x & ((1 << log_tpr) - 1);
+  const int pr = (int)(blockIdx.x - n_join) * (256 >> log_tpr) + (threadIdx.x >> log_tpr);
+  const int routed_rows = p.B * p.G * p.rows_pad;
+  if (pr >= (int)p.n_rows_pad) return;
   gqe_bf16_t* dst;
   if (pr < routed_rows) {
-    const int sq = (int)(pr / p.rows_pad), r = (int)(pr % p.rows_pad);
+    const int sq = pr / p.rows_pad, r = pr - sq * p.rows_pad;
     if (r >= p.T * p.k) return;
     dst = p.dq_routed + ((long long)sq * p.T * p.k + r) * p.d;
   } else {
-    const long long q2 = pr - routed_rows;
-    const int b = (int)(q2 / p.rows_pad_sh), r = (int)(q2 % p.rows_pad_sh);
+    const int b = (pr - routed_rows) / p.rows_pad_sh, r = pr - routed_rows - b * p.rows_pad_sh;
     if (r >= p.T) return;
     dst = p.dq_sh + ((long long)b * p.T + r) * p.d;
   }
-  const float4* a = reinterpret_cast<const float4*>(p.dq_acc + pr * p.d + part * 8);
+  const float4* a = reinterpret_cast<const float4*>(p.dq_acc + (size_t)pr * p.d + part * 8);
   const float4 x = a[0], y = a[1];
   const float f = p.scale;
   reinterpret_cast<uint4*>(dst)[part] = make_uint4(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f),
