@@ -273,7 +273,7 @@ def gqe_window_workspace_size(dims, op, L_max=0, window=0, sinks=0) -> int:
     """Scratch bytes of the windowed and tree calls (may be 0)."""
     n = _SZ(0)
     _check("gqe_window_workspace_size", lib.gqe_window_workspace_size(
-        ctypes.byref(dims), op, int(L_max), int(window), int(sinks), ctypes.byref(n)))
+        ctypes.byref(dims), op, int(L_max), _bound(window), _bound(sinks), ctypes.byref(n)))
     return int(n.value)
 
 
@@ -302,6 +302,12 @@ def _lens(t, name, n, dev, optional=False):
     return p
 
 
+def _bound(v):
+    """A window or a number of sinks as the C int the call takes: 2^31 - 1 tokens
+    are more than any sequence has, and a negative one stays negative."""
+    return max(-1, min(int(v), 0x7FFFFFFF))
+
+
 def _scratch(ws, dev):
     """Pointer and size of a scratch tensor that may be absent."""
     return (None, 0) if ws is None else (_dev(ws, "ws", ws.dtype, dev), ws.numel() * ws.element_size())
@@ -311,7 +317,7 @@ def gqe_attn_prefill_window(dims, q_routed, q_sh, K, V, window, sinks, o_routed,
     dev = torch.cuda.current_device()
     _check("gqe_attn_prefill_window", lib.gqe_attn_prefill_window(
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
-        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), int(window), int(sinks),
+        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), _bound(window), _bound(sinks),
         _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True),
         _dev(lse, "lse", _F32, dev, True), _stream(stream, dev)))
 
@@ -322,7 +328,7 @@ def gqe_attn_prefill_window_bwd(dims, q_routed, q_sh, K, V, window, sinks, o_rou
     wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_prefill_window_bwd", lib.gqe_attn_prefill_window_bwd(
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
-        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), int(window), int(sinks),
+        _dev(K, "K", _BF16, dev), _dev(V, "V", _BF16, dev), _bound(window), _bound(sinks),
         _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True),
         _dev(lse, "lse", _F32, dev), _dev(do_routed, "do_routed", _BF16, dev),
         _dev(do_sh, "do_sh", _BF16, dev, True), _dev(dq_routed, "dq_routed", _BF16, dev),
@@ -337,8 +343,8 @@ def gqe_attn_decode_window(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, windo
     _check("gqe_attn_decode_window", lib.gqe_attn_decode_window(
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
         _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev), int(L_max),
-        _lens(cache_len, "cache_len", dims.B, dev), int(window), int(sinks), _dev(o_routed, "o_routed", _BF16, dev),
-        _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes, _stream(stream, dev)))
+        _lens(cache_len, "cache_len", dims.B, dev), _bound(window), _bound(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes, _stream(stream, dev)))
 
 
 def gqe_attn_tree(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max, cache_len, window, sinks, o_routed,
@@ -351,7 +357,7 @@ def gqe_attn_tree(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max,
         ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev), _dev(q_sh, "q_sh", _BF16, dev, True),
         _dev(Kt, "Kt", _BF16, dev), _dev(Vt, "Vt", _BF16, dev), _lens(parent, "parent", dims.B * dims.T, dev),
         _lens(tree_len, "tree_len", dims.B, dev, True), _dev(Kc, "Kc", _BF16, dev), _dev(Vc, "Vc", _BF16, dev),
-        int(L_max), _lens(cache_len, "cache_len", dims.B, dev), int(window), int(sinks),
+        int(L_max), _lens(cache_len, "cache_len", dims.B, dev), _bound(window), _bound(sinks),
         _dev(o_routed, "o_routed", _BF16, dev), _dev(o_sh, "o_sh", _BF16, dev, True), wp, ws_bytes,
         _stream(stream, dev)))
 

@@ -170,6 +170,80 @@ def test_window_backward_dK_dV_are_deterministic():
     assert torch.equal(a[2], b[2]) and torch.equal(a[3], b[3])
 
 
+@pytest.mark.parametrize("window,sinks", [(700, 3), (0, 0)])
+def test_window_backward_in_rounds(window, sinks):
+    """A batch whose dq sums (69 MB) are worked on in two rounds of stretches:
+    the sequences at both ends and on both sides of the rounds' border."""
+    dims = D(B=32, T=1400, G=2, k=1, d=128)
+    plain = gq.gqe_workspace_size(gq.make_dims(dims), gq.GQE_OP_ATTN_BWD)
+    need = gq.gqe_window_workspace_size(gq.make_dims(dims), gq.GQE_OP_ATTN_WINDOW_BWD, 0, window, sinks)
+    assert need > plain + 148 * 2 * 2 * 128 * 128 * 4 + 256
+    x = _prefill_inputs(dims, 16)
+    do, dos = gi.normal_bf16(16, "do", x["q"].shape), gi.normal_bf16(16, "dosh", x["qs"].shape)
+    dev, o, os_, lse = _run_prefill(dims, x, window, sinks)
+    got = _run_bwd(dims, dev, window, sinks, o, os_, lse, bf16_dev(do), bf16_dev(dos))
+    for t in got:
+        assert torch.isfinite(t).all()
+    keep = [0, 15, 16, 31]
+    R, R_sh = dims.G * dims.T, dims.B * dims.G * dims.T
+    lse = torch.cat([lse[b * R:(b + 1) * R] for b in keep] + [lse[R_sh + b * 1400:R_sh + (b + 1) * 1400] for b in keep])
+    x = {n: v[keep] for n, v in x.items()}
+    ref, bnd = ow.attn_prefill_window_bwd(x["q"], x["qs"], x["K"], x["V"], window, sinks, to_f64(lse), do[keep],
+                                          dos[keep], dims.replace(B=4))
+    for name, t, r, b in zip(("dq", "dq_sh", "dK", "dV"), got, ref, bnd):
+        close(t[keep], r, b, name)
+
+
+def test_window_backward_replayed_from_one_graph():
+    """The schedule travels with the launch: replays follow new inputs in the same tensors."""
+    dims, window, sinks = BWD["few_and_many"]
+    x, y = _prefill_inputs(dims, 18), _prefill_inputs(dims, 19)
+    do, dos = bf16_dev(gi.normal_bf16(18, "do", x["q"].shape)), bf16_dev(gi.normal_bf16(18, "dosh", x["qs"].shape))
+    dev, o, os_, lse = _run_prefill(dims, x, window, sinks)
+    dq, dK, dV, dqs = (full(*t.shape) for t in (o, dev["K"], dev["K"], os_))
+    ws = full(gq.gqe_window_workspace_size(gq.make_dims(dims), gq.GQE_OP_ATTN_WINDOW_BWD, 0, window, sinks) // 4,
+              dtype=torch.float32)
+
+    def step():
+        gq.gqe_attn_prefill_window(gq.make_dims(dims), dev["q"], dev["qs"], dev["K"], dev["V"], window, sinks, o, os_,
+                                   lse)
+        gq.gqe_attn_prefill_window_bwd(gq.make_dims(dims), dev["q"], dev["qs"], dev["K"], dev["V"], window, sinks, o,
+                                       os_, lse, do, dos, dq, dqs, dK, dV, ws)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for n in dev:
+        dev[n].copy_(bf16_dev(y[n]))
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    dev2, o2, os2, lse2 = _run_prefill(dims, y, window, sinks)
+    _, _, dK2, dV2 = _run_bwd(dims, dev2, window, sinks, o2, os2, lse2, do, dos)
+    assert torch.equal(o, o2) and torch.equal(dK, dK2) and torch.equal(dV, dV2)
+
+
+def test_bounds_past_32_bits_do_not_wrap():
+    dims, _, _ = PREFILL["window_over_T"]
+    x = _prefill_inputs(dims, 20)
+    _, a, _, _ = _run_prefill(dims, x, 0, 0)
+    _, b, _, _ = _run_prefill(dims, x, 2 ** 32 + 5, 2 ** 33)
+    assert torch.equal(a, b)
+    with pytest.raises(gq.GQEError):
+        _run_prefill(dims, x, -2 ** 32 + 5, 0)
+    dims, L, lens, _, _ = DECODE["no_window"]
+    x = _cache_inputs(dims, L, 21)
+    dev = {n: None if v is None else bf16_dev(v) for n, v in x.items()}
+    outs = []
+    for w, s in ((0, 0), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 40)):
+        o, os_ = full(*dev["q"].shape), full(*dev["qs"].shape)
+        gq.gqe_attn_decode_window(gq.make_dims(dims), dev["q"], dev["qs"], dev["Kc"], dev["Vc"], L, i32(lens), w, s, o,
+                                  os_)
+        outs.append(o)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 @pytest.mark.parametrize("case", ["window_one", "one_token"])
 def test_one_visible_key_has_no_score_gradient(case):
     dims, window, sinks = PREFILL[case]
