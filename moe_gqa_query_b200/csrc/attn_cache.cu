@@ -36,7 +36,7 @@
 // Bound by HBM where there are many keys: 64 sequences under a 4096-token window
 // (d = 64, 8 groups) 90 us, 0.92 of the measured copy bandwidth; 64 trees of 32
 // tokens over 32768-token caches 675 us, 0.99.  Few keys: by latency, start 3 us,
-// about 1 us a key tile, join 2-3 us (one tree of 8 tokens, 4096 rows: 10.3 us).
+// about 1 us a key tile, join 2-3 us (one tree of 8 tokens, 4096 rows: 10.0 us).
 #include "attn.cuh"
 #include "launch.cuh"
 
@@ -600,7 +600,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
 
 // Accepted drafted rows to the end of the cache: one CTA per sequence, so that
 // new_len may be cache_len itself (the CTA has read it before it writes).  Bound by
-// latency (lengths, path, row, one after the other): 2.6 us for one sequence, 4.6
+// latency (lengths, path, row, one after the other): 2.0 us for one sequence, 3.5
 // us for 64 sequences of 17 rows of 8 groups, of which the bytes are 0.3 us.
 __global__ void __launch_bounds__(512) cache_commit_kernel(CommitParams p) {
   pdl_launch_dependents();
@@ -653,9 +653,9 @@ void cache_attn_plan(int B, int T, int G, int k, int n_shared, int d, int L_max,
   // 1 us): start-up and end 5, a tile 4/3 when two CTAs share an SM, a quarter
   // for each CTA of the cluster's barriers, all of it once per 296 CTAs (two on
   // each of 148 SMs) but at least once.  Measured (us): 64 x 8 items of 33 tiles
-  // 95, 109, 121 for 1, 2, 3 shares; 20 items of 17 tiles 14.2, 11.2, 9.9, 11.2,
-  // 19 for 2, 4, 6, 8, 16; 72 items of 35 tiles 36, 33, 51 for 2, 3, 4; 8 items
-  // of 33 tiles 20, 14.6, 11.7, 11.7 for 2, 4, 6, 16.
+  // 95, 109, 121 for 1, 2, 3 shares; 20 items of 17 tiles 12.7, 10.0, 8.8, 10.0
+  // for 2, 4, 6, 8; 72 items of 35 tiles 43, 27, 25, 28, 36 for 1, 2, 3, 4, 6; 8
+  // items of 33 tiles 16.8, 12.2, 10.4, 10.0 for 2, 4, 6, 8.
   const long long items = (long long)B * G * P->n_qt, nt = max_tiles(L_max, T, tree, window, sinks, KT);
   const int cap = (int)(nt < 16 ? nt : 16);
   double best = 0;
