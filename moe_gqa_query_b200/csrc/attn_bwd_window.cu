@@ -826,7 +826,9 @@ attn_bwd_window_post_kernel(const __grid_constant__ AttnBwdParams p, const __gri
 // window / 128 + 2 times, from DRAM if all sequences are worked on at once (2 x
 // 8192 tokens, 17 heads of d = 128, 143 MB of sums: 3.3 GB of DRAM traffic in one
 // round), so rounds of at most 64 MB of sums, while a stretch keeps 16 query
-// tiles (a cut costs two fp32 tiles written and read).
+// tiles (a cut costs two fp32 tiles written and read): 0.87 GB, 556 -> 491 us.
+// Parts of the batch in launches of their own, so that the sums are zeroed and
+// rounded in L2 too, lost to this by their ramps (760 against 746 us a step).
 constexpr long long kRoundBytes = 64 << 20;
 
 void attn_bwd_window_plan(int B, int T, int G, int k, int n_shared, int sg, int d, int window, int sinks,
