@@ -524,14 +524,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         // both warpgroups hold their S^T columns in registers before warpgroup 1
         // writes P^T over warpgroup 0's; every thread of the two warpgroups
         // passes here each tile and they leave together if any wait failed
-        int any_fail;
-        asm volatile(
-            "{\n\t.reg .pred q, r;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-            "bar.red.or.pred r, 1, 256, q;\n\tselp.b32 %0, 1, 0, r;\n\t}"
-            : "=r"(any_fail)
-            : "r"((int)!ok)
-            : "memory");
-        if (any_fail) break;
+        if (bar_or<1, 256>(!ok)) break;
       }
       {
         uint32_t pk[32];

@@ -70,6 +70,20 @@ __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ---------------------------------------------------------------- named barrier
+// Barrier ID of N threads (whole warps): true for all of them if any brings true.
+template <int ID, int N>
+__device__ __forceinline__ bool bar_or(bool pred) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred q, r;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "bar.red.or.pred r, %2, %3, q;\n\tselp.b32 %0, 1, 0, r;\n\t}"
+      : "=r"(any)
+      : "r"((int)pred), "n"(ID), "n"(N)
+      : "memory");
+  return any != 0;
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
