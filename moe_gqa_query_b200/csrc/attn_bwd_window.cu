@@ -585,20 +585,25 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
     uint8_t* stage = smem + C::OffEpi + qd * C::EpiCh * 4096;
     uint32_t N = 0;
     do {
-      // A key tile's last query tile: dK and dV first at d = 64 (they are done
-      // before dQ is), so that the next key tile's products into them start; at
-      // d = 128 the next dP^T waits for the dQ drain, so that comes first.
+      // dq_full comes first, at a key tile's last query tile too.  These warps wait for
+      // dk_done and pv_done only there, and a wait's parity means phase N only once
+      // phase N-1 is over, which dq_full(N) implies: the warps that made dS(N) had
+      // passed pv_done(N-1) (d = 64) or dk_done(N-1) (d = 128), and dP(N) or S(N) was
+      // issued behind the other one.  (Phase N+1 waits for acc_free.)
+      if (!wait(&bar->dq_full, N)) break;
+      tc_fence_after();
+      // A key tile's last query tile: dK and dV first at d = 64, so that the next key
+      // tile's products into them start; at d = 128 the next dP^T waits for the dQ
+      // drain, so that comes first.
 #pragma unroll 1
       for (int step = 0; step < 2; ++step) {
         if ((step == 0) != C::kWide) {
           if (!c.last()) continue;
-          if (!wait(&bar->pv_done, N) || !wait(&bar->dk_done, N)) goto out;
+          if (!wait(&bar->dk_done, N) || !wait(&bar->pv_done, N)) goto out;
           tc_fence_after();
           read_acc<D>(c, p, tmem + lane_off, qd * 32 + lane, &bar->acc_free);
           continue;
         }
-        if (!wait(&bar->dq_full, N)) goto out;
-        tc_fence_after();
         const int row_pad = c.row_pad(p);
         // the whole row at once, so that the columns are free again soon (d = 128:
         // dP^T(N+1) waits for them)
