@@ -404,7 +404,12 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
   const int rep = n_rows <= 32 ? 4 : n_rows <= 64 ? 2 : 1;
   const int lanes_rep = kRowsQ / rep;
 
-  pdl_launch_dependents();
+  // Tensor memory first (an empty share's CTA too): a dependent CTA may start on this
+  // SM at the signal and allocate columns that it keeps while it waits for this grid.
+  if (warp == 5) {
+    tmem_alloc(&sh->tmem_base, 256);
+    pdl_launch_dependents();
+  }
   pdl_wait();
   if (tid == 0 && blockIdx.x % (p.n_split * p.n_qt) == 0 && g == 0 && p.err) {
     const int n = p.cache_len[b];
@@ -457,7 +462,6 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
         if (j < VST) load_v(j);
       }
     }
-    if (warp == 5) tmem_alloc(&sh->tmem_base, 256);
     const int up = p.tree && tid < cl.m ? p.parent[(size_t)b * p.T + tid] : -1;
     // Q rows, repeated `rep` times, into the 128-byte swizzled layout (every load
     // in flight before the first store: one trip to memory)
@@ -588,10 +592,10 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
-      tc_fence_after();
-      tmem_dealloc(tmem, 256);
-    }
+  }
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(sh->tmem_base, 256);
   }
   join_shares<D>(p, sh, smem, rows, row0, n_rows);
   report_abort(abort, p.err, kErrTimeoutCacheAttn);

@@ -536,7 +536,10 @@ gemm_routed_kernel(const __grid_constant__ CUtensorMap mapWq, const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int K = rp.K;
   const int nk = K / kBK;
-  pdl_launch_dependents();
+  if (warp == 1) {
+    tmem_alloc(&bar->tmem_base, kTmemCols);
+    pdl_launch_dependents();      // behind the allocation: a dependent's could take its columns
+  }
   pdl_wait();
   for (int i = threadIdx.x; i < rp.n_seg; i += blockDim.x) {
     const int c = rp.seg_cnt[i];
@@ -571,7 +574,6 @@ gemm_routed_kernel(const __grid_constant__ CUtensorMap mapWq, const __grid_const
     tma_prefetch_desc(&mapWq);
     tma_prefetch_desc(&mapWsh);
   }
-  if (warp == 1) tmem_alloc(&bar->tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -639,8 +639,10 @@ __global__ void __launch_bounds__(224, 1) router_tc_kernel(const __grid_constant
     tma_prefetch_desc(&mapX);
     tma_prefetch_desc(&mapW);
   }
-  if (warp == 1) tmem_alloc(&bar->tmem_base, kTmemCols);
-  pdl_launch_dependents();
+  if (warp == 1) {
+    tmem_alloc(&bar->tmem_base, kTmemCols);
+    pdl_launch_dependents();      // behind the allocation: a dependent's could take its columns
+  }
   pdl_wait();
   for (int e = threadIdx.x; e < GEP; e += blockDim.x) sBias[e] = (p.bias && e < GE) ? p.bias[e] : 0.f;
   tc_fence_before();
