@@ -404,12 +404,6 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
   const int rep = n_rows <= 32 ? 4 : n_rows <= 64 ? 2 : 1;
   const int lanes_rep = kRowsQ / rep;
 
-  // Tensor memory first (an empty share's CTA too): a dependent CTA may start on this
-  // SM at the signal and allocate columns that it keeps while it waits for this grid.
-  if (warp == 5) {
-    tmem_alloc(&sh->tmem_base, 256);
-    pdl_launch_dependents();
-  }
   pdl_wait();
   if (tid == 0 && blockIdx.x % (p.n_split * p.n_qt) == 0 && g == 0 && p.err) {
     const int n = p.cache_len[b];
@@ -422,12 +416,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
   const int first = (int)((long long)cl.n * share / p.n_split);
   const int n = rows.token(row0) < cl.m ? (int)((long long)cl.n * (share + 1) / p.n_split) - first : 0;
 
-  if (n == 0) {
-    // an empty share: its rows saw nothing
-    if (tid < n_rows) sh->row_ml[tid] = make_float2(-INFINITY, 0.f);
-    if (tid == 0) sh->abort = 0;
-    __syncthreads();
-  } else {
+  if (n > 0) {
     auto load_k = [&](int j) {
       const int s = j % KST, i = first + j;
       const CUtensorMap* map = i < cl.n_cache ? &mapK : &mapKt;
@@ -462,6 +451,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
         if (j < VST) load_v(j);
       }
     }
+    if (warp == 5) tmem_alloc(&sh->tmem_base, 256);
     const int up = p.tree && tid < cl.m ? p.parent[(size_t)b * p.T + tid] : -1;
     // Q rows, repeated `rep` times, into the 128-byte swizzled layout (every load
     // in flight before the first store: one trip to memory)
@@ -488,6 +478,9 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
+    // Behind the allocation: a dependent CTA may start on this SM at the signal, and
+    // allocate columns that it keeps while it waits for this grid.
+    pdl_launch_dependents();
 
     if (warp == 4) {
       const bool leader = elect_one();
@@ -592,10 +585,16 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-  }
-  if (warp == 5) {
-    tc_fence_after();
-    tmem_dealloc(sh->tmem_base, 256);
+    if (warp == 5) {
+      tc_fence_after();
+      tmem_dealloc(tmem, 256);
+    }
+  } else {
+    pdl_launch_dependents();
+    // an empty share: its rows saw nothing
+    if (tid < n_rows) sh->row_ml[tid] = make_float2(-INFINITY, 0.f);
+    if (tid == 0) sh->abort = 0;
+    __syncthreads();
   }
   join_shares<D>(p, sh, smem, rows, row0, n_rows);
   report_abort(abort, p.err, kErrTimeoutCacheAttn);
