@@ -295,9 +295,9 @@ def _dev(t, name, dtype, dev, optional=False):
 
 def _lens(t, name, n, dev, optional=False):
     """_dev of an int32 tensor of exactly n entries (lengths, parents, paths: a
-    narrower one would be read past its end)."""
+    narrower one would be read past its end), or a device pointer as it is."""
     p = _dev(t, name, _I32, dev, optional)
-    if p is not None and t.numel() != n:
+    if p is not None and not isinstance(t, int) and t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
     return p
 
