@@ -124,8 +124,3 @@ def test_windowed_config_values():
     for bad in (dict(window=-1), dict(sinks=-1)):
         with pytest.raises(ValueError):
             gq.GQEConfig(**base, **bad)
-
-
-def test_binding_takes_device_pointers_for_lengths_too():
-    assert _lib._lens(4096, "cache_len", 3, 0) == 4096
-    assert _lib._lens(None, "tree_len", 3, 0, True) is None
