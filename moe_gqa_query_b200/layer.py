@@ -60,6 +60,17 @@ def config_from(obj) -> GQEConfig:
                         if hasattr(obj, f.name)})
 
 
+def check_cache(cfg, B: int, Kc: torch.Tensor, Vc: torch.Tensor) -> int:
+    """The row count L_max of a cache pair [B, G, L_max, d] (more sequences than
+    B are left alone).  Raises for one that the calls would read or write at
+    other places than its owner means."""
+    if Kc.shape != Vc.shape:
+        raise ValueError(f"Kc {tuple(Kc.shape)} and Vc {tuple(Vc.shape)} differ")
+    if Kc.dim() != 4 or Kc.shape[0] < B or Kc.shape[1] != cfg.G or Kc.shape[3] != cfg.d:
+        raise ValueError(f"cache {tuple(Kc.shape)} is not [{B}, {cfg.G}, L_max, {cfg.d}]")
+    return Kc.shape[2]
+
+
 class GQELayer:
     """Holds a layer's weights on one GPU and runs its forward passes."""
 
@@ -350,7 +361,7 @@ class GQELayer:
         int32 on the device.  Returns y [B, D]."""
         c = self.cfg
         B = x_new.shape[0]
-        L_max = Kc.shape[2]
+        L_max = check_cache(c, B, Kc, Vc)
         dims = L.make_dims(c, B=B, T=1)
         idx = self._buf("d_idx", (B, c.G, c.k), torch.int32)
         w = self._buf("d_w", (B, c.G, c.k), torch.float32)
@@ -393,7 +404,7 @@ class GQELayer:
         rows past tree_len of y hold nothing of use.  The cache is read only."""
         c = self.cfg
         B, T = x_draft.shape[0], x_draft.shape[1]
-        L_max = Kc.shape[2]
+        L_max = check_cache(c, B, Kc, Vc)
         dims = L.make_dims(c, B=B, T=T)
         N = B * T
         idx = self._buf("t_idx", (N, c.G, c.k), torch.int32)
@@ -425,7 +436,8 @@ class GQELayer:
         cache: path [B, T] int32 (drafted tokens in order), n_accept [B] int32.
         The new lengths go to new_len, or into cache_len itself without one."""
         Kt, Vt = draft["K"], draft["V"]
+        L_max = check_cache(self.cfg, Kt.shape[0], Kc, Vc)
         dims = L.make_dims(self.cfg, B=Kt.shape[0], T=Kt.shape[2])
         new_len = cache_len if new_len is None else new_len
-        L.gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, Kc.shape[2], cache_len, new_len, stream)
+        L.gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, L_max, cache_len, new_len, stream)
         return new_len

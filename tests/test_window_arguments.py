@@ -92,3 +92,37 @@ def test_a_cache_length_past_32_bits_is_refused(call):
     run, _ = call
     with pytest.raises(ValueError, match="elements"):
         run("gqe_attn_tree", {8: lambda v: v + 2 ** 32})
+
+
+def test_layer_looks_at_its_cache():
+    """decode_step, decode_tree and commit take L_max from the cache and the rest of its shape from
+    the layer and the batch: the two must agree."""
+    from moe_gqa_query_b200.layer import check_cache
+    cfg = gq.GQEConfig(B=B, T=T, D=64, G=G, E=2, k=k, d=d)
+    new = lambda *s: torch.zeros(*s, dtype=BF16)  # noqa: E731
+    assert check_cache(cfg, B, new(*CACHE), new(*CACHE)) == L
+    assert check_cache(cfg, B, new(B + 3, G, L, d), new(B + 3, G, L, d)) == L      # the first B sequences of a larger one
+    for bad in ((B - 1, G, L, d), (B, G - 1, L, d), (B, G + 1, L, d), (B, G, L, 2 * d), (B, G * L, d)):
+        with pytest.raises(ValueError, match="cache"):
+            check_cache(cfg, B, new(*bad), new(*bad))
+    with pytest.raises(ValueError, match="differ"):
+        check_cache(cfg, B, new(*CACHE), new(B, G, L + 1, d))
+
+
+@pytest.mark.parametrize("step", ["decode_step", "decode_tree", "commit"])
+def test_layer_refuses_a_cache_before_it_launches_anything(monkeypatch, step):
+    from moe_gqa_query_b200 import layer as mod
+    for name in ("gqe_router_topk", "gqe_routed_qproj", "gqe_kv_append", "gqe_kv_proj", "gqe_cache_commit"):
+        monkeypatch.setattr(mod.L, name, lambda *a: pytest.fail("launched"))
+    self = object.__new__(mod.GQELayer)
+    self.cfg = gq.GQEConfig(B=B, T=T, D=64, G=G, E=2, k=k, d=d, window=4)
+    new = lambda *s: torch.zeros(*s, dtype=BF16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=I32)  # noqa: E731
+    Kc, Vc = new(B, G - 1, L, d), new(B, G - 1, L, d)
+    with pytest.raises(ValueError, match="cache"):
+        if step == "decode_step":
+            self.decode_step(new(B, 64), Kc, Vc, i32(B))
+        elif step == "decode_tree":
+            self.decode_tree(new(B, T, 64), i32(B, T), Kc, Vc, i32(B))
+        else:
+            self.commit(dict(K=new(*KV), V=new(*KV)), i32(B, T), i32(B), Kc, Vc, i32(B))
