@@ -487,10 +487,10 @@ gqe_status gqe_layer_forward_host(const gqe_dims* dims, const gqe_layer_weights*
 /* Reads and clears the device error word (0 = none).  Kernels set it when one
  * of their internal waits runs out of time (0x101 GEMM, 0x201 attention,
  * 0x202 attention backward, 0x301 decode, 0x303 tree and windowed decode,
- * 0x401 router, 0x7F1 the failure check below), when a decode or tree call
- * meets a cache_len outside its range (0x302), gqe_attn_tree a tree_len or
- * parent outside its range (0x304) or gqe_cache_commit a value outside its
- * range (0x305).  The first code recorded is kept.  Synchronises
+ * 0x401 router, 0x7F1 and 0x7F2 the failure checks below), when a decode or
+ * tree call meets a cache_len outside its range (0x302), gqe_attn_tree a
+ * tree_len or parent outside its range (0x304) or gqe_cache_commit a value
+ * outside its range (0x305).  The first code recorded is kept.  Synchronises
  * `stream`. */
 gqe_status gqe_device_error(int* code, gqe_stream stream);
 
@@ -500,6 +500,9 @@ gqe_status gqe_device_error(int* code, gqe_stream stream);
  * word (read and cleared by gqe_device_error) and returns: the context stays
  * usable.  No fault, no trap. */
 gqe_status gqe_debug_wait_timeout(gqe_stream stream);
+/* The same through the waits of the windowed and tree kernels, which count
+ * tries (about one second of them): code 0x7F2. */
+gqe_status gqe_debug_wait_short_timeout(gqe_stream stream);
 
 /* Diagnostics.  Evaluates the attention kernel's exponential helpers on n
  * fp32 inputs (device arrays): y_poly the polynomial exp2 used on the FMA

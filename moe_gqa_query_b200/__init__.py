@@ -17,5 +17,6 @@ from ._lib import (  # noqa: F401
     GQE_OP_ATTN_WINDOW_BWD, GQE_OP_ATTN_DECODE_WINDOW, GQE_OP_ATTN_TREE, gqe_window_workspace_size,
     gqe_attn_prefill_window, gqe_attn_prefill_window_bwd, gqe_attn_decode_window, gqe_attn_tree, gqe_cache_commit,
     gqe_status_string, gqe_debug_exp2, gqe_debug_wait_timeout,
+    gqe_debug_wait_short_timeout,
 )
 from .layer import GQEConfig, GQELayer  # noqa: F401

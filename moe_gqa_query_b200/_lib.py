@@ -106,6 +106,7 @@ SIGNATURES = {
     "gqe_device_error": [ctypes.POINTER(_I), _P],
     "gqe_debug_exp2": [_P, _P, _P, _P, _I, _P],
     "gqe_debug_wait_timeout": [_P],
+    "gqe_debug_wait_short_timeout": [_P],
     "gqe_status_string": [_I],
 }
 
@@ -560,6 +561,11 @@ def gqe_device_error(stream=None) -> int:
 
 def gqe_debug_wait_timeout(stream=None):
     _check("gqe_debug_wait_timeout", lib.gqe_debug_wait_timeout(_stream(stream)))
+
+
+def gqe_debug_wait_short_timeout(stream=None):
+    """The same through the windowed and tree kernels' waits: code 0x7F2."""
+    _check("gqe_debug_wait_short_timeout", lib.gqe_debug_wait_short_timeout(_stream(stream)))
 
 
 def gqe_debug_exp2(x, y_poly, y_pair, y_hw, stream=None):

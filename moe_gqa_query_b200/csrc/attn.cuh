@@ -25,6 +25,7 @@ struct AttnParams {
 
 // diag.cu: a bounded wait that runs out (failure-path test)
 cudaError_t launch_debug_wait(unsigned* err, cudaStream_t stream);
+cudaError_t launch_debug_wait_short(unsigned* err, cudaStream_t stream);
 
 cudaError_t launch_attn_prefill(const CUtensorMap& mQ, const CUtensorMap& mQs, const CUtensorMap& mK,
                                 const CUtensorMap& mV, const AttnParams& p, int d,

@@ -32,7 +32,38 @@ __global__ void debug_wait_kernel(unsigned* err) {
   }
 }
 
+// The same through the waits of the windowed and tree kernels: warp 0 waits
+// as a warp, warp 1 as single threads, first on a barrier that is complete, then on
+// one that nothing arrives at.  The code is recorded only if every thread passed the
+// first and gave up on the second.
+__global__ void debug_wait_short_kernel(unsigned* err) {
+  __shared__ uint64_t bar[2];
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar[0], 64);
+    mbar_init(&bar[1], 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  volatile int* abort = &abort_flag;
+  auto wait = [&](uint64_t* b) {
+    return threadIdx.x < 32 ? mbar_wait_warp(b, 0, abort) : mbar_wait_short(b, 0, abort);
+  };
+  mbar_arrive(&bar[0]);
+  const bool passed = wait(&bar[0]);
+  const bool gave_up = passed && !wait(&bar[1]);
+  const bool all = __syncthreads_and(gave_up);
+  report_abort(abort, all ? err : nullptr, kErrTimeoutDebugShort);
+  drain_after_abort(abort);
+}
+
 }  // namespace
+
+cudaError_t launch_debug_wait_short(unsigned* err, cudaStream_t stream) {
+  debug_wait_short_kernel<<<1, 64, 0, stream>>>(err);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_debug_wait(unsigned* err, cudaStream_t stream) {
   debug_wait_kernel<<<1, 32, 0, stream>>>(err);

@@ -1029,6 +1029,12 @@ gqe_status gqe_debug_wait_timeout(gqe_stream stream) {
   return cuda_status(launch_debug_wait(err, S(stream)));
 }
 
+gqe_status gqe_debug_wait_short_timeout(gqe_stream stream) {
+  unsigned* err = error_word();
+  GQE_REQUIRE(err, GQE_ERR_CUDA);
+  return cuda_status(launch_debug_wait_short(err, S(stream)));
+}
+
 gqe_status gqe_device_error(int* code, gqe_stream stream) {
   GQE_REQUIRE(code, GQE_ERR_INVALID_ARG);
   unsigned v = 0;
