@@ -474,6 +474,9 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
     const uint32_t col0 = (uint32_t)(wg * 64);
     const unsigned long long sl2x2 = f2_pack(p.scale_log2, p.scale_log2);
     uint32_t N = 0;
+    // d = 128: a thread whose wait failed goes on to the next tile's vote, where all of
+    // the two warpgroups leave together; the others would wait for it there
+    bool ok = true;
     do {
       const int st = N & 1;
       const int kv_pos = c.jt * kTileW + r, kk = c.shared() ? 1 : p.k, base = c.qi(p) * kTileW + (int)col0;
@@ -481,8 +484,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
       // tokens whose window starts behind it
       const int cmin = kv_pos * kk - base;
       const int cmax = kv_pos < p.sinks ? kTileW : (kv_pos + p.window) * kk - base;
-      bool ok = wait(&bar->q_full[st], N >> 1);
-      ok = ok && wait(&bar->s_full, N);
+      ok = ok && wait(&bar->q_full[st], N >> 1) && wait(&bar->s_full, N);
       if (!C::kWide && !ok) break;
       tc_fence_after();
       const float* lse2 = sLse + st * 128 + col0;
@@ -522,8 +524,7 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         tc_fence_after();
       } else {
         // both warpgroups hold their S^T columns in registers before warpgroup 1
-        // writes P^T over warpgroup 0's; every thread of the two warpgroups
-        // passes here each tile and they leave together if any wait failed
+        // writes P^T over warpgroup 0's
         if (bar_or<1, 256>(!ok)) break;
       }
       {
@@ -536,7 +537,11 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
       tc_fence_before();
       mbar_arrive(&bar->p_full);
 
-      if (!wait(&bar->dp_full, N)) break;
+      ok = wait(&bar->dp_full, N);
+      if (!ok) {
+        if (C::kWide) continue;
+        break;
+      }
       tc_fence_after();
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
@@ -569,7 +574,10 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
           st_shared_v4(atom + (((ch * 4 + j) ^ (r & 7)) << 4), dsk[j * 4], dsk[j * 4 + 1], dsk[j * 4 + 2],
                        dsk[j * 4 + 3]);
       }
-      if (!ok) break;
+      if (!ok) {
+        if (C::kWide) continue;
+        break;
+      }
       if (!C::kWide) tmem_wait_st();
       fence_proxy_async_smem();
       tc_fence_before();

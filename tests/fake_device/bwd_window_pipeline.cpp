@@ -10,11 +10,14 @@
 //    overwritten, dK and dV when the products of all the walk's pairs, and none of
 //    the next walk's, are in them;
 //  - no stage of shared memory is written while something still reads it;
-//  - all pairs are done, and no wait is left that nothing completes.
+//  - all pairs are done, and no wait is left that nothing completes;
+//  - when a copy or a commit is lost, or a wait runs out too early, the CTA still ends,
+//    with the abort flag raised.
 //
 // usage: bwd_window_pipeline d B T G k n_shared sg window sinks trials seed mode
 // mode: what is late: copies, commits, products, reads (of the staging
-// buffers) or nothing.
+// buffers) or nothing; lost_copy, lost_commit: one of them, another in each trial, never
+// comes; timeout: a wait runs out at some step of each trial.
 // Prints the first fault and its trial; exit code 1 then.
 #include "sm100.cuh"
 
@@ -257,7 +260,7 @@ struct Model {
     }
   }
 
-  static bool trial(int cta) {
+  static bool trial(int cta, bool losing) {
     list(cta);
     boxes.clear();
     s_done = dp_done = dv_steps = dk_steps = dq_steps = s_steps = dp_steps = bulk_landed = 0;
@@ -270,6 +273,18 @@ struct Model {
     });
     const int n = (int)pairs.size();
     fake::current = -1;
+    if (ok && losing) {
+      const int flag = reinterpret_cast<BwdWinBarriers*>(smem_raw + C::OffBar)->abort;
+      if (fake::aborted != (flag != 0) || (!fake::aborted && fake::lose < 0 && fake::timeout_at < 0)) {
+        fake::error = "a lost event and no abort";
+        return false;
+      }
+      return true;
+    }
+    if (ok && fake::aborted) {
+      fake::error = "a wait ran out";
+      return false;
+    }
     if (ok && !(s_done == n && dp_done == n && dv_steps == 8 * n && dk_steps == 8 * n && dq_steps == 8 * n &&
                 all(dq_reads, 12, 16, n) && all(dk_reads, 12, 16, (int)item_end.size() * D / 32) &&
                 all(dv_reads, 12, 16, (int)item_end.size() * D / 32))) {
@@ -329,7 +344,11 @@ int main(int argc, char** argv) {
     if (mode == "products") fake::weight[fake::kProduct] = 0.02;
     if (mode == "reads") fake::weight[fake::kRead] = slow;
     const int cta = (int)(fake::rng() % (unsigned)sched.n_ctas);
-    const bool ok = wide ? Model<128>::trial(cta) : Model<64>::trial(cta);
+    const bool losing = mode == "lost_copy" || mode == "lost_commit" || mode == "timeout";
+    fake::lose_kind = mode == "lost_copy" ? fake::kCopy : fake::kCommit;
+    fake::lose = mode != "timeout" && losing ? (int)(fake::rng() % 60u) : -1;
+    fake::timeout_at = mode == "timeout" ? (long)(fake::rng() % 6000u) : -1;
+    const bool ok = wide ? Model<128>::trial(cta, losing) : Model<64>::trial(cta, losing);
     if (!ok) {
       printf("trial %d, CTA %d of %d, %d pairs in %d walks: %s\n", t, cta, sched.n_ctas, (int)pairs.size(),
              (int)item_end.size(), fake::error.c_str());

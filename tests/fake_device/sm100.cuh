@@ -7,6 +7,9 @@
 //    that every lane makes counts 32.  Any fiber that is not blocked may run next.
 //  - mbarriers have PTX's phases: a wait for a parity returns when the phase of
 //    that parity is the last completed one, whichever phase the caller means.
+//  - when nothing else can happen (or at a step that the harness chooses), a wait runs
+//    out: it raises the kernel's abort flag, and the checks on data stop, but the warps
+//    must still all come to the end.
 //  - copies land, products run and commits arrive as events of their own, at any
 //    time after they were issued: a thread's products run in the order of issue, a
 //    commit's arrival comes at any time after the thread's earlier products, and the
@@ -52,6 +55,7 @@ struct Fiber {
   std::vector<char> stack;
   bool done = false;
   std::function<bool()> blocked_on;          // empty: runnable
+  volatile int* abort = nullptr;             // in a bounded wait: the flag it raises when it runs out
   std::deque<std::function<bool()>> queue;   // products (false) and commits (true) issued, in order
   int reads = 0;                             // bulk stores that still read shared memory
 };
@@ -67,8 +71,14 @@ inline std::string error;
 inline std::vector<uint8_t> smem;            // the CTA's shared memory, 1024-byte aligned at `base`
 inline uint8_t* base = nullptr;
 
+inline bool aborted = false;                 // some wait has run out
+inline int lose = -1;                        // the copy or commit that never comes
+inline int lose_kind = kCopy;
+inline long timeout_at = -1;                 // step at which a wait runs out although it would have ended
+inline bool lost(int kind) { return kind == lose_kind && lose-- == 0; }
+
 inline void fail(const std::string& what) {
-  if (error.empty()) error = "warp " + std::to_string(current) + ": " + what;
+  if (error.empty() && !aborted) error = "warp " + std::to_string(current) + ": " + what;
 }
 inline void yield() { swapcontext(&fibers[current].ctx, &main_ctx); }
 inline void block(std::function<bool()> until) {
@@ -129,6 +139,7 @@ inline bool run_cta(int n, std::function<void()> body) {
   barriers.clear();
   meets.clear();
   error.clear();
+  aborted = false;
   for (Fiber& f : fibers) {
     f.stack.resize(256 * 1024);
     getcontext(&f.ctx);
@@ -157,15 +168,27 @@ inline bool run_cta(int n, std::function<void()> body) {
       if (!f.queue.empty()) offer(kProduct, i);
     }
     for (size_t i = 0; i < events.size(); ++i) offer(events[i].kind, (int)i);
-    if (can.empty()) {
-      if (!all_done) {
-        std::string who;
-        for (int i = 0; i < n; ++i)
-          if (!fibers[i].done) who += " " + std::to_string(i);
-        current = -1;
-        fail("stuck: nothing can happen, warps" + who + " wait");
+    if (can.empty() && all_done) break;
+    const bool early = timeout_at >= 0 && timeout_at-- == 0;
+    if (can.empty() || early) {
+      std::vector<int> waits;
+      std::string who;
+      for (int i = 0; i < n; ++i)
+        if (!fibers[i].done) {
+          who += " " + std::to_string(i);
+          if (fibers[i].abort) waits.push_back(i);
+        }
+      if (waits.empty() && can.empty()) {
+        error = "stuck: warps" + who + " wait for what nothing brings";
+        break;
       }
-      break;
+      if (waits.empty()) {
+        timeout_at = 0;      // at the next step, then
+      } else {
+        aborted = true;
+        *fibers[waits[rng() % waits.size()]].abort = 1;
+        continue;
+      }
     }
     double x = std::uniform_real_distribution<double>(0, total)(rng);
     size_t c = 0;
@@ -246,9 +269,12 @@ inline void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
   fake::arrive(bar, 1, bytes);
   fake::settle(bar);
 }
-inline bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int*) {
-  fake::block([bar, parity] { return fake::passed(bar, parity); });
-  return true;
+inline bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const int who = fake::current;
+  fake::fibers[who].abort = abort;
+  fake::block([=] { return fake::passed(bar, parity) || *abort; });
+  fake::fibers[who].abort = nullptr;
+  return fake::passed(bar, parity);
 }
 inline bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return mbar_wait_short(bar, parity, abort);
@@ -267,6 +293,7 @@ inline void tma_prefetch_desc(const CUtensorMap*) {}
 inline void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
   const uint32_t d = smem_u32(dst);
   fake::on_copy(d, map, c0, c1, c2, false);
+  if (fake::lost(fake::kCopy)) return;
   fake::events.push_back({fake::kCopy, [=] {
                             fake::on_copy(d, map, c0, c1, c2, true);
                             fake::barriers[bar].tx -= 128 * 128;
@@ -318,6 +345,7 @@ inline void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t, uint32_t accum
   });
 }
 inline void umma_commit(uint64_t* bar) {
+  if (fake::lost(fake::kCommit)) return;
   fake::fibers[fake::current].queue.push_back([=] {
     fake::events.push_back({fake::kCommit, [=] {
                               fake::arrive(bar, 1);

@@ -13,7 +13,8 @@ with one kind of them made much later than the rest.  Every product, every read 
 write of tensor memory and every reuse of shared memory is checked against the list
 of (key tile, query tile) pairs that the CTA stands for.
 
-Waits taken out of a copy of the source must be caught.
+Waits taken out of a copy of the source must be caught.  And when a wait runs out,
+the kernel has to end.
 """
 import os
 import shutil
@@ -77,6 +78,15 @@ def test_every_pair_meets_its_own_tiles(pipeline, case, late):
     rc, out = run(pipeline, case, 100, late)
     assert rc == 0, out
     assert ("2 rounds" in out) == case.endswith("two_rounds")
+
+
+@pytest.mark.parametrize("fault", ["lost_copy", "lost_commit", "timeout"])
+@pytest.mark.parametrize("case", ["ragged", "one_pair_walks", "d128_ragged", "d128_one_pair_walks"])
+def test_a_wait_that_runs_out_ends_the_kernel(pipeline, case, fault):
+    """A copy or a commit never comes, or a wait runs out while the others still go on: every warp
+    must come to the end, none may stay at a barrier that has no limit."""
+    rc, out = run(pipeline, case, 400, fault)
+    assert rc == 0, out
 
 
 # a wait taken out of the source, where it must show
