@@ -275,11 +275,11 @@ struct Model {
     fake::current = -1;
     if (ok && losing) {
       const int flag = reinterpret_cast<BwdWinBarriers*>(smem_raw + C::OffBar)->abort;
-      if (fake::aborted != (flag != 0) || (!fake::aborted && fake::lose < 0 && fake::timeout_at < 0)) {
-        fake::error = "a lost event and no abort";
+      if (fake::aborted != (flag != 0)) {
+        fake::error = "a wait ran out and the abort flag is down";
         return false;
       }
-      return true;
+      if (fake::aborted) return true;       // else nothing waited for what was lost: all must be done
     }
     if (ok && fake::aborted) {
       fake::error = "a wait ran out";
