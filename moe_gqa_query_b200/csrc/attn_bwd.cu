@@ -340,10 +340,12 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
     const uint32_t col0 = (uint32_t)(wg * 64);
     const float scale = p.scale;
     bool ok = true;
-    for (int n = 0; n < cnt && ok; ++n) {
+    // d = 128: a thread whose wait failed goes on to the next tile's vote, where all of
+    // the two warpgroups leave together; the others would wait for it there
+    for (int n = 0; n < cnt && (C::kWide || ok); ++n) {
       const int st = n & 1;
       const QTile q = qtile(p, s, jt, n_r, n);
-      ok = mbar_wait(&bar->q_full[st], (n >> 1) & 1, abort, p.err, kErrTimeoutAttnBwd);
+      ok = ok && mbar_wait(&bar->q_full[st], (n >> 1) & 1, abort, p.err, kErrTimeoutAttnBwd);
       ok = ok && mbar_wait(&bar->s_full, n & 1, abort, p.err, kErrTimeoutAttnBwd);
       if (!C::kWide && !ok) break;
       tc_fence_after();
@@ -384,16 +386,8 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
       }
       if (C::kWide) {
         // both warpgroups hold their S^T columns in registers before warpgroup 1
-        // writes P^T over warpgroup 0's; every thread of the two warpgroups
-        // passes here each tile and they leave together if any wait failed
-        int any_fail;
-        asm volatile(
-            "{\n\t.reg .pred q, r;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-            "bar.red.or.pred r, 1, 256, q;\n\tselp.b32 %0, 1, 0, r;\n\t}"
-            : "=r"(any_fail)
-            : "r"((int)!ok)
-            : "memory");
-        if (any_fail) break;
+        // writes P^T over warpgroup 0's
+        if (bar_or<1, 256>(!ok)) break;
       }
       {
         uint32_t pk[32];
@@ -406,7 +400,10 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
       mbar_arrive(&bar->p_full);
 
       ok = mbar_wait(&bar->dp_full, n & 1, abort, p.err, kErrTimeoutAttnBwd);
-      if (!ok) break;
+      if (!ok) {
+        if (C::kWide) continue;
+        break;
+      }
       tc_fence_after();
       // dP^T chunks of 16 columns.  d = 128: the next chunk's load in flight
       // while this one is used (measured faster there, slower at d = 64)

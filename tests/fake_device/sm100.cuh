@@ -1,5 +1,5 @@
 // sm100.cuh (stand-in) -- test infrastructure, host only.  The device wrappers of
-// csrc/sm100.cuh that the windowed backward uses, over a small model of one CTA,
+// csrc/sm100.cuh that the attention's backward kernels use, over a small model of one CTA,
 // so that a kernel's roles run on a machine without a GPU and the order of their
 // waits can be checked under any timing:
 //
@@ -276,6 +276,9 @@ inline bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort)
   fake::fibers[who].abort = nullptr;
   return fake::passed(bar, parity);
 }
+inline bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned*, unsigned) {
+  return mbar_wait_short(bar, parity, abort);
+}
 inline bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return mbar_wait_short(bar, parity, abort);
 }
@@ -362,6 +365,10 @@ inline void tmem_ld(uint32_t a, uint32_t* r) {
   memset(r, 0, N * 4);
   fake::yield();
 }
+inline void tmem_ld16(uint32_t a, uint32_t* r) { tmem_ld<16>(a, r); }
+inline void tmem_ld16_async(uint32_t a, uint32_t* r) { tmem_ld<16>(a, r); }
+inline void tmem_wait_ld16(uint32_t*) {}
+inline void tmem_st8(uint32_t a, const uint32_t*) { fake::on_tmem_store(a & 0xFFFFu, 8); }
 inline void tmem_ld32(uint32_t a, uint32_t* r) { tmem_ld<32>(a, r); }
 inline void tmem_ld64(uint32_t a, uint32_t* r) { tmem_ld<64>(a, r); }
 inline void tmem_st16(uint32_t a, const uint32_t*) { fake::on_tmem_store(a & 0xFFFFu, 16); }
