@@ -529,10 +529,10 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant_
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    drain_after_abort(abort);      // what is in flight lands before another CTA gets the columns
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  drain_after_abort(abort);
 }
 
 // Delta_r = sum_c dO_rc O_rc and LSE2_r = LSE_r * log2(e) into the padded row

@@ -650,11 +650,11 @@ attn_bwd_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    drain_after_abort(abort);      // what is in flight lands before another CTA gets the columns
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
   report_abort(abort, p.err, kErrTimeoutAttnBwd);
-  drain_after_abort(abort);
 }
 
 __device__ __forceinline__ float dot8(uint4 a, uint4 b) {

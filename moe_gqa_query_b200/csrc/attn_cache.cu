@@ -586,6 +586,7 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
     tc_fence_before();
     __syncthreads();
     if (warp == 5) {
+      drain_after_abort(abort);      // what is in flight lands before another CTA gets the columns
       tc_fence_after();
       tmem_dealloc(tmem, 256);
     }
@@ -598,7 +599,6 @@ attn_cache_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constan
   }
   join_shares<D>(p, sh, smem, rows, row0, n_rows);
   report_abort(abort, p.err, kErrTimeoutCacheAttn);
-  drain_after_abort(abort);
 }
 
 // Accepted drafted rows to the end of the cache: one CTA per sequence, so that

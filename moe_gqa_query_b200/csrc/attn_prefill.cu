@@ -394,10 +394,10 @@ attn_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_const
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
+    drain_after_abort(abort);      // what is in flight lands before another CTA gets the columns
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  drain_after_abort(abort);
 }
 
 // ---------------------------------------------------------------------------
@@ -754,10 +754,10 @@ attn_prefill_single_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
   __syncthreads();
   ATTN_TRACE(if (TR && threadIdx.x == 0) TR[9] = globaltimer();)
   if (warp == 5) {
+    drain_after_abort(abort);      // what is in flight lands before another CTA gets the columns
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
-  drain_after_abort(abort);
 }
 
 }  // namespace

@@ -354,12 +354,12 @@ attn_prefill_window_kernel(const __grid_constant__ CUtensorMap mapQ, const __gri
   tc_fence_before();
   __syncthreads();
   if (warp == 4) {
+    drain_after_abort(abort);      // what is in flight lands before another CTA gets the columns
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
     if (C::kApart) tmem_dealloc(tmem_p, 32);
   }
   report_abort(abort, p.err, kErrTimeoutAttn);
-  drain_after_abort(abort);
 }
 
 }  // namespace

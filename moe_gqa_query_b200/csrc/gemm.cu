@@ -302,10 +302,10 @@ gemm_dense_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constan
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    drain_after_abort(abort);      // what is in flight lands before another CTA gets the columns
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  drain_after_abort(abort);
 }
 
 // ---------------------------------------------------------------------------
@@ -675,10 +675,10 @@ gemm_routed_kernel(const __grid_constant__ CUtensorMap mapWq, const __grid_const
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    drain_after_abort(abort);      // what is in flight lands before another CTA gets the columns
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  drain_after_abort(abort);
 }
 
 }  // namespace

@@ -737,10 +737,10 @@ __global__ void __launch_bounds__(224, 1) router_tc_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    drain_after_abort(abort);      // what is in flight lands before another CTA gets the columns
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  drain_after_abort(abort);
 }
 
 template <int GEP, int STAGES>

@@ -73,3 +73,12 @@ def test_tensor_memory_before_the_signal(file, name, body):
 ])
 def test_the_rule_itself(body, good):
     assert signals_behind_the_allocation(body) == good
+
+
+@pytest.mark.parametrize("file,name,body", FOUND, ids=[f"{f}:{n}" for f, n, _ in FOUND])
+def test_an_aborted_cta_lets_its_products_land_before_it_frees_their_columns(file, name, body):
+    """After a wait has run out products may still be in flight: freed columns could be another
+    kernel's by the time they are written."""
+    free = re.search(r"\btmem_dealloc\w*\(", body)
+    land = re.search(r"\bdrain_after_abort\(", body)
+    assert free and land and land.start() < free.start()
