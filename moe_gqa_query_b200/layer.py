@@ -98,6 +98,7 @@ class GQELayer:
         self.Wo = dev(weights["Wo"], (c.D, c.slots * c.d))
         self.bias = None if bias is None else torch.as_tensor(bias, dtype=torch.float32).to(self.device).contiguous()
         self._bufs = {}
+        self._captured = {}
         self._graphs = {}
         self._side = None
         self.concurrent_kv = True
@@ -108,6 +109,9 @@ class GQELayer:
         if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
             t = torch.empty(shape, dtype=dtype, device=self.device)
             self._bufs[name] = t
+        if torch.cuda.is_current_stream_capturing():
+            # a graph holds the buffer's address: it stays when a call of another shape takes its name
+            self._captured[t.data_ptr()] = t
         return t
 
     def _ws(self, name, nbytes):
