@@ -203,8 +203,8 @@ gqe_status gqe_attn_prefill_window(const gqe_dims* dims, const gqe_bf16* q_route
  *   ws: gqe_window_workspace_size(GQE_OP_ATTN_WINDOW_BWD) bytes, 256-byte
  *   aligned.
  * Errors: GQE_ERR_UNSUPPORTED for 2^31 rows or more, each sequence's rows of a
- * group counted in tiles of 128 (its scratch would be 137 GB), else as
- * gqe_attn_prefill_bwd. */
+ * group counted in tiles of 128 (the scratch, 4 d + 8 bytes a row, would be 567
+ * GB at d = 64), else as gqe_attn_prefill_bwd. */
 gqe_status gqe_attn_prefill_window_bwd(const gqe_dims* dims, const gqe_bf16* q_routed, const gqe_bf16* q_sh,
                                        const gqe_bf16* K, const gqe_bf16* V, int window, int sinks,
                                        const gqe_bf16* o_routed, const gqe_bf16* o_sh, const float* lse,

@@ -126,3 +126,13 @@ def test_layer_refuses_a_cache_before_it_launches_anything(monkeypatch, step):
             self.decode_tree(new(B, T, 64), i32(B, T), Kc, Vc, i32(B))
         else:
             self.commit(dict(K=new(*KV), V=new(*KV)), i32(B, T), i32(B), Kc, Vc, i32(B))
+
+
+def test_scratch_of_the_windowed_backward_is_4d_plus_8_bytes_a_row():
+    """dq's fp32 sums, -LSE2 and -Delta of every row of the padded space; 2^31 rows, which are refused,
+    would take 567 GB at d = 64."""
+    for width, most in ((64, 570e9), (128, 1.12e12)):
+        dims = gq.gqe_dims(B=(1 << 24) - 1, T=1, d_model=64, G=1, E=1, k=1, d_head=width, n_shared=0,
+                           shared_kv_group=0, renorm_scope=0, scale=0.0, output_mode=0)
+        need = gq.gqe_window_workspace_size(dims, gq.GQE_OP_ATTN_WINDOW_BWD, 0, 0, 0)
+        assert 128 * dims.B * (4 * width + 8) <= need <= most
