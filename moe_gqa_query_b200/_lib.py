@@ -281,34 +281,33 @@ def gqe_window_workspace_size(dims, op, L_max=0, window=0, sinks=0) -> int:
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
+# The checks below are half of a small call's host time, so the tensors that pass
+# them do so in one expression.
+_Tensor = torch.Tensor
+
+
 def _dev(t, name, dtype, dev, optional=False, n=0):
     """_ptr for the calls below, which also refuse a tensor of another device
     than the current one, dev (the library launches on the current device), or
     of fewer than the n elements that the call reads or writes (a device pointer
     is taken as it is)."""
+    if type(t) is _Tensor and t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
     if t is None and optional:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        if t.numel() < n:
-            raise ValueError(f"{name} has {t.numel()} elements, the call needs {n}")
-        return t.data_ptr()
+    if isinstance(t, _Tensor) and t.get_device() == dev and t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, the call needs {n}")
     p = _ptr(t, name, dtype)
-    if isinstance(t, torch.Tensor):
+    if isinstance(t, _Tensor) and t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
     return p
-
-
-def _counts(dims):
-    """Elements of the routed rows, the shared head's rows and the K (or V) rows
-    of dims.T tokens, and values of the log-sum-exp."""
-    B, T, G, d = dims.B, dims.T, dims.G, dims.d_head
-    kv = B * G * T * d
-    return kv * dims.k, B * T * d * dims.n_shared, kv, B * T * (G * dims.k + dims.n_shared)
 
 
 def _lens(t, name, n, dev, optional=False):
     """_dev of an int32 tensor of exactly n entries (lengths, parents, paths: a
     narrower one would be read past its end), or a device pointer as it is."""
+    if type(t) is _Tensor and t.dtype is _I32 and t.get_device() == dev and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
     p = _dev(t, name, _I32, dev, optional)
     if p is not None and not isinstance(t, int) and t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
@@ -318,7 +317,7 @@ def _lens(t, name, n, dev, optional=False):
 def _bound(v):
     """A window or a number of sinks as the C int the call takes: 2^31 - 1 tokens
     are more than any sequence has, and a negative one stays negative."""
-    return max(-1, min(int(v), 0x7FFFFFFF))
+    return v if type(v) is int and -1 <= v <= 0x7FFFFFFF else max(-1, min(int(v), 0x7FFFFFFF))
 
 
 def _scratch(ws, dev):
@@ -326,43 +325,55 @@ def _scratch(ws, dev):
     return (None, 0) if ws is None else (_dev(ws, "ws", ws.dtype, dev), ws.numel() * ws.element_size())
 
 
+# Elements below: nq of the routed rows, ns of the shared head's, nk of the K (or V)
+# rows of dims.T tokens, nc of a cache, nl values of the log-sum-exp.
+
 def gqe_attn_prefill_window(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse=None, stream=None):
     dev = torch.cuda.current_device()
-    nq, ns, nk, nl = _counts(dims)
+    nt, nk, G, k, sh = dims.B * dims.T, dims.d_head, dims.G, dims.k, dims.n_shared
+    ns, nl = nt * nk * sh, nt * (G * k + sh)
+    nk *= nt * G
+    nq = nk * k
     _check("gqe_attn_prefill_window", lib.gqe_attn_prefill_window(
-        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev, n=nq), _dev(q_sh, "q_sh", _BF16, dev, True, ns),
-        _dev(K, "K", _BF16, dev, n=nk), _dev(V, "V", _BF16, dev, n=nk), _bound(window), _bound(sinks),
-        _dev(o_routed, "o_routed", _BF16, dev, n=nq), _dev(o_sh, "o_sh", _BF16, dev, True, ns),
+        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev, False, nq), _dev(q_sh, "q_sh", _BF16, dev, True, ns),
+        _dev(K, "K", _BF16, dev, False, nk), _dev(V, "V", _BF16, dev, False, nk), _bound(window), _bound(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev, False, nq), _dev(o_sh, "o_sh", _BF16, dev, True, ns),
         _dev(lse, "lse", _F32, dev, True, nl), _stream(stream, dev)))
 
 
 def gqe_attn_prefill_window_bwd(dims, q_routed, q_sh, K, V, window, sinks, o_routed, o_sh, lse, do_routed, do_sh,
                                 dq_routed, dq_sh, dK, dV, ws, stream=None):
     dev = torch.cuda.current_device()
-    nq, ns, nk, nl = _counts(dims)
+    nt, nk, G, k, sh = dims.B * dims.T, dims.d_head, dims.G, dims.k, dims.n_shared
+    ns, nl = nt * nk * sh, nt * (G * k + sh)
+    nk *= nt * G
+    nq = nk * k
     wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_prefill_window_bwd", lib.gqe_attn_prefill_window_bwd(
-        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev, n=nq), _dev(q_sh, "q_sh", _BF16, dev, True, ns),
-        _dev(K, "K", _BF16, dev, n=nk), _dev(V, "V", _BF16, dev, n=nk), _bound(window), _bound(sinks),
-        _dev(o_routed, "o_routed", _BF16, dev, n=nq), _dev(o_sh, "o_sh", _BF16, dev, True, ns),
-        _dev(lse, "lse", _F32, dev, n=nl), _dev(do_routed, "do_routed", _BF16, dev, n=nq),
-        _dev(do_sh, "do_sh", _BF16, dev, True, ns), _dev(dq_routed, "dq_routed", _BF16, dev, n=nq),
-        _dev(dq_sh, "dq_sh", _BF16, dev, True, ns), _dev(dK, "dK", _BF16, dev, n=nk), _dev(dV, "dV", _BF16, dev, n=nk),
-        wp, ws_bytes, _stream(stream, dev)))
+        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev, False, nq), _dev(q_sh, "q_sh", _BF16, dev, True, ns),
+        _dev(K, "K", _BF16, dev, False, nk), _dev(V, "V", _BF16, dev, False, nk), _bound(window), _bound(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev, False, nq), _dev(o_sh, "o_sh", _BF16, dev, True, ns),
+        _dev(lse, "lse", _F32, dev, False, nl), _dev(do_routed, "do_routed", _BF16, dev, False, nq),
+        _dev(do_sh, "do_sh", _BF16, dev, True, ns), _dev(dq_routed, "dq_routed", _BF16, dev, False, nq),
+        _dev(dq_sh, "dq_sh", _BF16, dev, True, ns), _dev(dK, "dK", _BF16, dev, False, nk),
+        _dev(dV, "dV", _BF16, dev, False, nk), wp, ws_bytes, _stream(stream, dev)))
 
 
 def gqe_attn_decode_window(dims, q_routed, q_sh, Kc, Vc, L_max, cache_len, window, sinks, o_routed, o_sh, ws=None,
                            stream=None):
     dev = torch.cuda.current_device()
-    L_max = int(L_max)
-    nq, ns, nk, _ = _counts(dims)
-    nc = dims.B * dims.G * dims.d_head * L_max
+    B, ns, L_max = dims.B, dims.d_head, int(L_max)
+    ns *= B
+    nc = ns * dims.G
+    nq = nc * dims.k
+    nc *= L_max
+    ns *= dims.n_shared
     wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_decode_window", lib.gqe_attn_decode_window(
-        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev, n=nq), _dev(q_sh, "q_sh", _BF16, dev, True, ns),
-        _dev(Kc, "Kc", _BF16, dev, n=nc), _dev(Vc, "Vc", _BF16, dev, n=nc), L_max,
-        _lens(cache_len, "cache_len", dims.B, dev), _bound(window), _bound(sinks),
-        _dev(o_routed, "o_routed", _BF16, dev, n=nq), _dev(o_sh, "o_sh", _BF16, dev, True, ns), wp, ws_bytes,
+        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev, False, nq), _dev(q_sh, "q_sh", _BF16, dev, True, ns),
+        _dev(Kc, "Kc", _BF16, dev, False, nc), _dev(Vc, "Vc", _BF16, dev, False, nc), L_max,
+        _lens(cache_len, "cache_len", B, dev), _bound(window), _bound(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev, False, nq), _dev(o_sh, "o_sh", _BF16, dev, True, ns), wp, ws_bytes,
         _stream(stream, dev)))
 
 
@@ -371,17 +382,20 @@ def gqe_attn_tree(dims, q_routed, q_sh, Kt, Vt, parent, tree_len, Kc, Vc, L_max,
     """Attention of dims.T drafted tokens per sequence over the cache and over
     their tree (parent [B, T] int32, tree_len [B] int32 or None)."""
     dev = torch.cuda.current_device()
-    L_max = int(L_max)
-    nq, ns, nk, _ = _counts(dims)
-    nc = dims.B * dims.G * dims.d_head * L_max
+    B, T, ns, L_max = dims.B, dims.T, dims.d_head, int(L_max)
+    nc = B * dims.G * ns * L_max
+    ns *= B * T
+    nk = ns * dims.G
+    nq = nk * dims.k
+    ns *= dims.n_shared
     wp, ws_bytes = _scratch(ws, dev)
     _check("gqe_attn_tree", lib.gqe_attn_tree(
-        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev, n=nq), _dev(q_sh, "q_sh", _BF16, dev, True, ns),
-        _dev(Kt, "Kt", _BF16, dev, n=nk), _dev(Vt, "Vt", _BF16, dev, n=nk),
-        _lens(parent, "parent", dims.B * dims.T, dev), _lens(tree_len, "tree_len", dims.B, dev, True),
-        _dev(Kc, "Kc", _BF16, dev, n=nc), _dev(Vc, "Vc", _BF16, dev, n=nc), L_max,
-        _lens(cache_len, "cache_len", dims.B, dev), _bound(window), _bound(sinks),
-        _dev(o_routed, "o_routed", _BF16, dev, n=nq), _dev(o_sh, "o_sh", _BF16, dev, True, ns), wp, ws_bytes,
+        ctypes.byref(dims), _dev(q_routed, "q_routed", _BF16, dev, False, nq), _dev(q_sh, "q_sh", _BF16, dev, True, ns),
+        _dev(Kt, "Kt", _BF16, dev, False, nk), _dev(Vt, "Vt", _BF16, dev, False, nk),
+        _lens(parent, "parent", B * T, dev), _lens(tree_len, "tree_len", B, dev, True),
+        _dev(Kc, "Kc", _BF16, dev, False, nc), _dev(Vc, "Vc", _BF16, dev, False, nc), L_max,
+        _lens(cache_len, "cache_len", B, dev), _bound(window), _bound(sinks),
+        _dev(o_routed, "o_routed", _BF16, dev, False, nq), _dev(o_sh, "o_sh", _BF16, dev, True, ns), wp, ws_bytes,
         _stream(stream, dev)))
 
 
@@ -389,14 +403,15 @@ def gqe_cache_commit(dims, Kt, Vt, path, n_accept, Kc, Vc, L_max, cache_len, new
     """Cache rows cache_len[b] .. += drafted rows path[b, :n_accept[b]];
     new_len (may be cache_len) = cache_len + n_accept."""
     dev = torch.cuda.current_device()
-    L_max = int(L_max)
-    nk = _counts(dims)[2]
-    nc = dims.B * dims.G * dims.d_head * L_max
+    B, T, nk, L_max = dims.B, dims.T, dims.G * dims.d_head, int(L_max)
+    nk *= B
+    nc = nk * L_max
+    nk *= T
     _check("gqe_cache_commit", lib.gqe_cache_commit(
-        ctypes.byref(dims), _dev(Kt, "Kt", _BF16, dev, n=nk), _dev(Vt, "Vt", _BF16, dev, n=nk),
-        _lens(path, "path", dims.B * dims.T, dev), _lens(n_accept, "n_accept", dims.B, dev),
-        _dev(Kc, "Kc", _BF16, dev, n=nc), _dev(Vc, "Vc", _BF16, dev, n=nc), L_max,
-        _lens(cache_len, "cache_len", dims.B, dev), _lens(new_len, "new_len", dims.B, dev), _stream(stream, dev)))
+        ctypes.byref(dims), _dev(Kt, "Kt", _BF16, dev, False, nk), _dev(Vt, "Vt", _BF16, dev, False, nk),
+        _lens(path, "path", B * T, dev), _lens(n_accept, "n_accept", B, dev), _dev(Kc, "Kc", _BF16, dev, False, nc),
+        _dev(Vc, "Vc", _BF16, dev, False, nc), L_max, _lens(cache_len, "cache_len", B, dev),
+        _lens(new_len, "new_len", B, dev), _stream(stream, dev)))
 
 
 def gqe_combine(dims, o_routed, o_sh, topk_w, h, stream=None):
