@@ -19,7 +19,8 @@
 // attn_bwd_window_post_kernel adds the slots of a walk in their order, so dK
 // and dV do not depend on timing.  dQ goes through TMA reduce-add into fp32 as
 // in attn_bwd.cu; with several stretches per CTA all CTAs work on one part of
-// the sequences at a time, so that the part's dQ sums stay in L2 (attn_bwd_window_plan).
+// the sequences at a time, so that the part's dQ sums stay in L2 (attn_bwd_window_plan:
+// up to 256 MB of them in all).
 //
 // CTA: 512 threads, roles, tensor memory and barriers as in attn_bwd.cu, with
 // every ring counted over the whole stretch, but for d = 128: dK reads dS from
@@ -832,7 +833,9 @@ attn_bwd_window_post_kernel(const __grid_constant__ AttnBwdParams p, const __gri
 // window / 128 + 2 times, from DRAM if all sequences are worked on at once (2 x
 // 8192 tokens, 17 heads of d = 128, 143 MB of sums: 3.3 GB of DRAM traffic in one
 // round), so rounds of at most 64 MB of sums, while a stretch keeps 16 query
-// tiles (a cut costs two fp32 tiles written and read): 0.87 GB, 556 -> 491 us.
+// tiles (a cut costs two fp32 tiles written and read): 0.87 GB, 556 -> 491 us.  There
+// are at most kBwdWindowRounds = 4 rounds, so with more than 256 MB of sums a round's
+// are more than 64 MB; what that costs is not measured.
 // Parts of the batch in launches of their own, so that the sums are zeroed and
 // rounded in L2 too, lost to this by their ramps (760 against 746 us a step).
 constexpr long long kRoundBytes = 64 << 20;

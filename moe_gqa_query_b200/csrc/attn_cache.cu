@@ -10,9 +10,10 @@
 // all of these at once: the cache's key tiles and the tree's are one list.
 //
 // The T*k routed rows of a group, and the shared head's T rows when the group
-// is the shared head's, are packed into 128-row query tiles, so each key tile
-// is read once for all of them.  Work item: one query tile of one (b, g) and a
-// share of its key list.  The CTAs of one query tile's shares form a cluster:
+// is the shared head's, are packed into 128-row query tiles; each query tile
+// reads the group's key tiles once (from L2 after the first, where a group has
+// more than 128 rows).  Work item: one query tile of one (b, g) and a share of its
+// key list.  The CTAs of one query tile's shares form a cluster:
 // each leaves its rows' softmax state (max, sum, unnormalised O, fp32) in its
 // own shared memory, and after a cluster barrier the CTAs divide the rows among
 // them and join the states over distributed shared memory.
@@ -258,9 +259,9 @@ struct RowMap {
 };
 
 // Ancestor bits and depths of the drafted tokens by pointer doubling, on the
-// 128 threads of the softmax warps: after round r a token's bits cover
-// 2^(r+1) - 1 levels above it.  up: thread i's parent[i].  Returns the buffer
-// that holds the result.
+// 128 threads of the softmax warps: a token starts with itself and one level, and
+// after round r = 0, 1, .. its bits cover the 2^(r+1) levels above it.  up: thread
+// i's parent[i].  Returns the buffer that holds the result.
 __device__ __forceinline__ int build_tree(const CacheAttnParams& p, const CacheList& cl, CacheShared* sh, int up) {
   const int i = threadIdx.x;
   if (up < -1 || up >= i) {
