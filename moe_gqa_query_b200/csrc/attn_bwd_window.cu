@@ -43,7 +43,7 @@
 // and -Delta, so a pair costs one FMA before its exponentials and one add and
 // one multiply after them; the scale of dS moves to where dK and dq are rounded.
 // What bounds the main kernel is each tile's chain S -> P, dP -> dS -> dQ, dK: 8 x
-// 2048 tokens of 9 heads, d = 64, under a 512-token window 103 us (0.24 of the
+// 2048 tokens of 9 heads, d = 64, under a 512-token window 102 us (0.24 of the
 // measured bf16 rate); 2 x 8192 tokens of 17 heads, d = 128, under 1024 tokens 491
 // us (0.42), where tensor memory is full and dP(i+1) waits for dQ(i)'s columns.
 // Exponentials on the FMA-pipe polynomial (2 or 4 of 16 pairs) changed the time

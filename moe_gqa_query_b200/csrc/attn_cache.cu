@@ -35,9 +35,10 @@
 // their V rows are zeroed in shared memory before P V reads them.
 //
 // Bound by HBM where there are many keys: 64 sequences under a 4096-token window
-// (d = 64, 8 groups) 90 us, 0.92 of the measured copy bandwidth; 64 trees of 32
-// tokens over 32768-token caches 675 us, 0.99.  Few keys: by latency, start 3 us,
-// about 1 us a key tile, join 2-3 us (one tree of 8 tokens, 4096 rows: 10.0 us).
+// (d = 64, 8 groups) 87 to 90 us, 0.92 to 0.96 of the measured copy bandwidth; 64
+// trees of 32 tokens over 32768-token caches 625 to 675 us, 0.99 and more.  Few keys:
+// by latency, start 3 us, about 1 us a key tile, join 2-3 us (one tree of 8 tokens,
+// 4096 rows: 10.1 us).  GPU times in a captured graph, by box.
 #include "attn.cuh"
 #include "launch.cuh"
 

@@ -20,8 +20,10 @@
 // 1024-token window: two CTAs with 128-key tiles 146 us, four with 64-key tiles
 // and P over S, so that S(j+1) waits for P(j) V, 146 us; this form 132 us (133
 // and 142 us with 2 and 4 of 16 pairs of exponentials on the FMA-pipe polynomial).
-// That is 0.34 of the measured bf16 rate; the exponential unit is 65 % busy and
-// bounds it.  2 x 8192 tokens of 17 heads at d = 128 take 171 us, 0.48 of it.
+// That is 0.34 of the measured bf16 rate; the exponential unit is 65 % busy, the
+// rest are the gaps that are left.  2 x 8192 tokens of 17 heads at d = 128 take 157
+// us, 0.52 of it.  (GPU times in a captured graph on one box; others: 131 to 138 us,
+// and 157 to 170.)
 //
 // With at most 32 sinks the sink tile is narrow: 32 of its keys take part in
 // S, the softmax and P V.
